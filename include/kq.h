@@ -65,7 +65,8 @@
  *                  K_params / K_f32 not 4-byte aligned;
  *   KQ_ERR_VARIANT unknown variant, or a variant whose inputs are missing
  *                  (KQ_MFMA_DENSE needs K_bf16; the others need K_params);
- *   KQ_ERR_ALIAS   an output range overlaps an input range or another output.
+ *   KQ_ERR_ALIAS   an output range overlaps an input range or another output;
+ *   KQ_ERR_WORKSPACE  a workspace is needed and NULL or too small.
  * tokens == 0 returns KQ_OK without touching the GPU.  A failed launch
  * returns KQ_ERR_HIP.  Faults inside a kernel surface at the caller's next
  * synchronization, as for any asynchronous HIP work.  No C++ exception
@@ -108,7 +109,8 @@ typedef enum {
   KQ_ERR_ALIGN = 3,
   KQ_ERR_VARIANT = 4,
   KQ_ERR_HIP = 5,
-  KQ_ERR_ALIAS = 6
+  KQ_ERR_ALIAS = 6,
+  KQ_ERR_WORKSPACE = 7
 } kq_status;
 
 /* How K is applied.  AUTO picks per shape: a kq_tune result if one was recorded, else the rule in kq_auto_variant. */
@@ -124,7 +126,7 @@ typedef enum {
 typedef enum { KQ_FRONT_KRON = 0, KQ_FRONT_PLAIN = 1, KQ_FRONT_SMOOTH = 2, KQ_FRONT_HADAMARD = 3 } kq_front;
 
 /* ABI version of this header (bumped on any signature or layout change). */
-#define KQ_ABI_VERSION 6
+#define KQ_ABI_VERSION 7
 int kq_abi_version(void);
 
 /* Static, never-NULL description of a status code. */
@@ -339,6 +341,117 @@ kq_status kq_build_blocks_inverse_t(const float* K_params, int64_t nb, float* K_
 kq_status kq_gemm_mx(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, const uint8_t* B_codes,
                      const uint8_t* B_scales, int64_t N, int64_t K, float* Y_f32, uint16_t* Y_bf16,
                      hipStream_t stream);
+
+/* Activations of kq_gemm_mx_ex. */
+typedef enum {
+  KQ_ACT_NONE = 0,
+  KQ_ACT_GELU_TANH = 1, /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+  KQ_ACT_GELU_ERF = 2,  /* x (1 + erf(x / sqrt 2)) / 2 */
+  KQ_ACT_SILU = 3       /* x / (1 + exp(-x)) */
+} kq_act;
+
+/*
+ * kq_gemm_mx with what a transformer layer does next on the fp32 sums, before
+ * the one rounding of the output: with s = sum_k a[m][k] b[n][k],
+ *   s = s + bias[n]                          if bias != NULL     (fp32 [N]);
+ *   s = act(s);
+ *   s = s * gate[m / rows_per_sample][n]     if gate != NULL     (fp32
+ *                      [ceil(M / rows_per_sample)][N], the AdaLN gate);
+ *   s = residual[m][n] + s                   if residual != NULL (bf16 [M][N]),
+ * in fp32 and in this order (an activation's absolute error is below 2^-21
+ * max(|x|, 1)).  Y_bf16 may be residual itself (the residual stream
+ * updated in place); any other overlap is KQ_ERR_ALIAS.  rows_per_sample is
+ * any positive number (KQ_ERR_SHAPE otherwise), read only with gate; an
+ * unknown act is KQ_ERR_VARIANT; bias and gate 4-byte, residual 2-byte
+ * aligned.  Otherwise as kq_gemm_mx; the sums may be formed in another order
+ * than kq_gemm_mx's (few rows split K over the waves of a workgroup), always
+ * the same one for the same sizes.
+ */
+kq_status kq_gemm_mx_ex(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, const uint8_t* B_codes,
+                        const uint8_t* B_scales, int64_t N, int64_t K, const float* bias, kq_act act,
+                        const float* gate, int64_t rows_per_sample, const uint16_t* residual, float* Y_f32,
+                        uint16_t* Y_bf16, hipStream_t stream);
+
+/*
+ * Key/value cache in MXFP4.  A cache is four pools with n_slots rows each:
+ * codes [n_slots][width/2] and E8M0 scales [n_slots][width/32] of keys and of
+ * values, row-major, width = kv_heads * head_dim (a multiple of 32; the 32
+ * channels of a block are consecutive in a row and may span two heads).  Row
+ * s is slot s, in the format kq_mx_quantize writes: a cache whose slots are in
+ * order can also be filled by any quantizer of this library.
+ *
+ * kq_cache_write quantizes rows t = 0 .. tokens - 1 of K (and of V, unless V
+ * is NULL) as kq_mx_quantize does and writes them to slot slots[t].  A token
+ * whose slot is outside [0, n_slots) (padding: -1) is not written; slots that
+ * no token names keep their contents.  Slots are meant to be distinct: of two
+ * tokens with the same slot either may be left there, block by block, codes
+ * and scales not necessarily from the same one.
+ *
+ * kq_cache_read writes the values of slot slots[t] to row t of K (and V):
+ * bf16(E2M1(code) * 2^(scale - 127)), exact for every scale this library
+ * writes (0 .. 252; above that a value past the bf16 range is infinite, and
+ * scale 255 reads as NaN).  A token whose slot is outside [0, n_slots) reads
+ * as zeros.  Slots may repeat.
+ *
+ * K and V are bf16 rows at strides K_stride and V_stride (elements; a multiple
+ * of 8, at least width), 16-byte aligned: columns of a wider matrix, such as a
+ * fused projection's output, serve as they are.  Codes 16-byte, scales and
+ * slots 4-byte aligned.  n_slots < 2^31; V's pools are not read when V is
+ * NULL.  One launch for both.
+ */
+kq_status kq_cache_write(const uint16_t* K, int64_t K_stride, const uint16_t* V, int64_t V_stride, int64_t tokens,
+                         int64_t width, const int32_t* slots, int64_t n_slots, uint8_t* K_codes, uint8_t* K_scales,
+                         uint8_t* V_codes, uint8_t* V_scales, hipStream_t stream);
+
+kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const uint8_t* V_codes,
+                        const uint8_t* V_scales, int64_t n_slots, int64_t width, const int32_t* slots, int64_t tokens,
+                        uint16_t* K, int64_t K_stride, uint16_t* V, int64_t V_stride, hipStream_t stream);
+
+/*
+ * Attention of bf16 queries over such a cache: for query i of a sequence and
+ * query head h, with key head h / (q_heads / kv_heads),
+ *   out = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j)
+ * over the keys j it sees.  The rule of precision: q, k and v enter the
+ * products unrounded, scores, maxima and sums are fp32, the probabilities
+ * (relative to the running maximum) are rounded once to bf16 before they
+ * multiply v, the output is rounded once.
+ *
+ * Queries: Q and out are bf16 [q_rows] rows of q_heads * head_dim at strides
+ * Q_stride and out_stride (elements, a multiple of 8), 16-byte aligned.
+ * Sequence b has rows q_start[b] .. q_start[b + 1] - 1 (int32 [batch + 1],
+ * not decreasing), or, with q_start NULL, rows b max_q .. (b + 1) max_q - 1.
+ * max_q bounds the queries of a sequence (<= q_rows); queries past it are not
+ * computed.  Ranges are cut to [0, q_rows).  Rows of out and lse that belong
+ * to no sequence are left as they are.
+ *
+ * Keys: sequence b has kv_len[b] of them (int32; cut to [0, pages_per_seq *
+ * page_size]).  Key j is at slot page_table[b][j / page_size] * page_size +
+ * j % page_size (int32 [batch][pages_per_seq]; pages may be shared), or, with
+ * page_table NULL, at slot b pages_per_seq page_size + j.  A key on a page
+ * outside [0, n_slots / page_size) is not there: as if masked.  page_size is
+ * any number from 1 to 2^24.  Nothing of a slot that no key names is used,
+ * whatever it holds.  causal != 0: with n queries and L keys, query i sees
+ * keys j <= L - n + i (the queries are the sequence's last tokens), else all
+ * L.  A query that sees no key gets out = 0 and lse = -infinity.
+ *
+ * head_dim is a multiple of 8 from 8 to 128, q_heads a multiple of kv_heads,
+ * scale positive and finite.  lse (fp32 [q_rows][q_heads]) may be NULL.
+ * Long key ranges with few queries are divided over workgroups and joined in
+ * a second launch; the partial results need kq_attention_mx_workspace bytes
+ * (0: none, workspace may be NULL), 16-byte aligned, free again when the call
+ * has run: calls that may run at the same time, two captured graphs among
+ * them, need one each.  The division depends on the sizes alone, so the same call gives
+ * the same bits.  capacity = pages_per_seq * page_size.
+ */
+int64_t kq_attention_mx_workspace(int64_t q_rows, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
+                                  int64_t head_dim, int64_t capacity);
+
+kq_status kq_attention_mx(const uint16_t* Q, int64_t Q_stride, int64_t q_rows, const int32_t* q_start, int64_t batch,
+                          int64_t max_q, const uint8_t* K_codes, const uint8_t* K_scales, const uint8_t* V_codes,
+                          const uint8_t* V_scales, int64_t n_slots, const int32_t* page_table, int64_t pages_per_seq,
+                          int64_t page_size, const int32_t* kv_len, int64_t q_heads, int64_t kv_heads,
+                          int64_t head_dim, float scale, int causal, uint16_t* out, int64_t out_stride, float* lse,
+                          void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * Measurement entry (not a quantizer): moves exactly the traffic of

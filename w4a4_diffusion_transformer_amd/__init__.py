@@ -10,6 +10,7 @@ or a tensor is not on the GPU, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -21,13 +22,15 @@ __all__ = [
     "kq_mx_quantize", "kq_smooth_quantize", "kq_hadamard_quantize", "kq_transform_f32",
     "alloc_outputs", "LIB_PATH", "kq_auto_variant", "variant_name", "kq_row_stats", "kq_quantize_adaln",
     "kq_build_blocks_inverse_t", "kq_gemm_mx", "kq_hadamard_quantize_ex", "kq_build_blocks16", "kq_tune",
-    "kq_tune_reset", "kq_stream_probe",
+    "kq_tune_reset", "kq_stream_probe", "KQ_ACT_NONE", "KQ_ACT_GELU_TANH", "KQ_ACT_GELU_ERF", "KQ_ACT_SILU",
+    "kq_gemm_mx_ex", "alloc_cache", "kq_cache_write", "kq_cache_read", "kq_attention_mx", "kq_attention_mx_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkq.so")
 
 KQ_AUTO, KQ_MFMA_DENSE, KQ_MFMA_OTF, KQ_BUTTERFLY = 0, 1, 2, 3
 KQ_FRONT_KRON, KQ_FRONT_PLAIN, KQ_FRONT_SMOOTH, KQ_FRONT_HADAMARD = 0, 1, 2, 3
+KQ_ACT_NONE, KQ_ACT_GELU_TANH, KQ_ACT_GELU_ERF, KQ_ACT_SILU = 0, 1, 2, 3
 VARIANTS = {"auto": KQ_AUTO, "mfma_dense": KQ_MFMA_DENSE, "mfma_otf": KQ_MFMA_OTF, "butterfly": KQ_BUTTERFLY}
 
 _lib = None
@@ -70,6 +73,16 @@ def lib() -> ctypes.CDLL:
         L.kq_tune_reset.argtypes = []
         L.kq_tune_reset.restype = None
         L.kq_quantize_adaln.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, i64, vp, ci, vp, vp, vp]
+        cf = ctypes.c_float
+        L.kq_gemm_mx_ex.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, ci, vp, i64, vp, vp, vp, vp]
+        L.kq_cache_write.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp]
+        L.kq_cache_read.argtypes = [vp, vp, vp, vp, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.kq_attention_mx.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64, vp, i64, i64, vp, i64, i64, i64,
+                                      cf, ci, vp, i64, vp, vp, i64, vp]
+        L.kq_attention_mx_workspace.argtypes = [i64] * 7
+        L.kq_attention_mx_workspace.restype = i64
+        for name in ("kq_gemm_mx_ex", "kq_cache_write", "kq_cache_read", "kq_attention_mx"):
+            getattr(L, name).restype = ci
         for name in ("kq_build_blocks", "kq_quantize", "kq_quantize_ex", "kq_mx_quantize", "kq_stream_probe",
                      "kq_smooth_quantize",
                      "kq_hadamard_quantize", "kq_transform_f32", "kq_row_stats", "kq_quantize_adaln",
@@ -277,3 +290,178 @@ def kq_tune(X, K_params, K_bf16, out_codes, out_scales, reps: int = 10, stream=N
 
 def kq_tune_reset() -> None:
     lib().kq_tune_reset()
+
+
+# The entry points below take strided rows, tables and several optional tensors: their tensors are checked
+# against one another here (the C ABI sees only addresses), have to be on one device, and run on that device.
+
+def _rows(t, what: str, width: int, rows: int):
+    """Address and row stride of a bf16 matrix [rows, width] whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: tensor must be on the GPU")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {_BF16}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{what}: expected [{rows}, {width}], got {list(t.shape)}")
+    stride = t.stride()
+    if stride[1] != 1 and width > 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.data_ptr(), stride[0] if rows > 1 else width
+
+
+def _full(t, what: str, dtype, shape):
+    """Address of a contiguous tensor of this type and shape (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{what}: tensor must be on the GPU")
+    if t.dtype not in dtype:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {list(shape)}, got {list(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _one_device(first, *others) -> int:
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return dev
+
+
+def _call(fn, where: str, dev: int, stream, *args):
+    """fn(*args, stream) on device `dev`: its current stream, or the one given."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, where, dev, stream, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        raise KQError(status, where)
+
+
+_I32 = (torch.int32,)
+
+
+def kq_gemm_mx_ex(a_codes, a_scales, b_codes, b_scales, bias=None, act: int = KQ_ACT_NONE, gate=None,
+                  rows_per_sample: int | None = None, residual=None, y_f32=None, y_bf16=None, stream=None):
+    """Y = residual + gate[m // rows_per_sample] * act(deq(A) deq(B)^T + bias); any of the three may be None.
+
+    bias float32 [N], gate float32 [samples, N] (rows_per_sample defaults to M: one sample), residual bfloat16
+    [M, N], which may be y_bf16 itself."""
+    M, half = a_codes.shape
+    N = b_codes.shape[0]
+    K = half * 2
+    rps = M if rows_per_sample is None else int(rows_per_sample)
+    if gate is not None and rps <= 0 < M:
+        raise ValueError("rows_per_sample must be positive")
+    dev = _one_device(a_codes, a_scales, b_codes, b_scales, bias, gate, residual, y_f32, y_bf16)
+    _call(lib().kq_gemm_mx_ex, "kq_gemm_mx_ex", dev, stream,
+          _full(a_codes, "a_codes", _U8, (M, half)), _full(a_scales, "a_scales", _U8, (M, K // 32)), M,
+          _full(b_codes, "b_codes", _U8, (N, half)), _full(b_scales, "b_scales", _U8, (N, K // 32)), N, K,
+          _full(bias, "bias", _F32, (N,)), int(act),
+          None if gate is None else _full(gate, "gate", _F32, (-(-M // rps) if M else gate.shape[0], N)), rps or 1,
+          _full(residual, "residual", _BF16, (M, N)), _full(y_f32, "y_f32", _F32, (M, N)),
+          _full(y_bf16, "y_bf16", _BF16, (M, N)))
+    return y_f32, y_bf16
+
+
+def alloc_cache(n_slots: int, width: int, device="cuda"):
+    """An empty MXFP4 key/value cache: (k_codes, k_scales, v_codes, v_scales), zeros."""
+    def zeros(w):
+        return torch.zeros((n_slots, w), dtype=torch.uint8, device=device)
+    return zeros(width // 2), zeros(width // 32), zeros(width // 2), zeros(width // 32)
+
+
+def _cache(k_codes, k_scales, v_codes, v_scales, width: int, both: bool = True):
+    """(n_slots, four addresses) of a cache's pools; the values' are None without `both`."""
+    n = k_codes.shape[0]
+    codes, scales = (n, width // 2), (n, width // 32)
+    if both:
+        v = (_full(v_codes, "v_codes", _U8, codes), _full(v_scales, "v_scales", _U8, scales))
+    else:
+        v = (None, None)
+    return n, (_full(k_codes, "k_codes", _U8, codes), _full(k_scales, "k_scales", _U8, scales)) + v
+
+
+def _cache_rows(K, V, slots):
+    T, W = K.shape
+    k, ks = _rows(K, "K", W, T)
+    v, vs = (None, W) if V is None else _rows(V, "V", W, T)
+    return T, W, k, ks, v, vs, _full(slots, "slots", _I32, (T,))
+
+
+def kq_cache_write(K, V, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
+    """Quantize rows of K and V (bfloat16 [tokens, width], V may be None) to MXFP4 and write them to their slots
+    (int32 [tokens], outside the cache: not written)."""
+    T, W, k, ks, v, vs, at = _cache_rows(K, V, slots)
+    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, W, V is not None)
+    dev = _one_device(K, V, slots, k_codes, k_scales, v_codes, v_scales)
+    _call(lib().kq_cache_write, "kq_cache_write", dev, stream, k, ks, v, vs, T, W, at, n, *pools)
+    return k_codes, k_scales, v_codes, v_scales
+
+
+def kq_cache_read(k_codes, k_scales, v_codes, v_scales, slots, K, V, stream=None):
+    """The values of slots (int32 [tokens], outside the cache: zeros) into K and V (bfloat16 [tokens, width], V may
+    be None)."""
+    T, W, k, ks, v, vs, at = _cache_rows(K, V, slots)
+    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, W, V is not None)
+    dev = _one_device(K, V, slots, k_codes, k_scales, v_codes, v_scales)
+    _call(lib().kq_cache_read, "kq_cache_read", dev, stream, *pools, n, W, at, T, k, ks, v, vs)
+    return K, V
+
+
+@functools.lru_cache(maxsize=1024)
+def kq_attention_mx_workspace(q_rows: int, batch: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
+                              capacity: int) -> int:
+    """Bytes of workspace that kq_attention_mx needs (0: none)."""
+    return int(lib().kq_attention_mx_workspace(q_rows, batch, max_q, q_heads, kv_heads, head_dim, capacity))
+
+
+def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_heads: int, kv_heads: int,
+                    page_size: int | None = None, pages_per_seq: int | None = None, page_table=None, q_start=None,
+                    max_q: int | None = None, scale: float | None = None, causal: bool = False, lse=None,
+                    workspace=None, stream=None):
+    """Attention of Q (bfloat16 [q_rows, q_heads * head_dim]) over an MXFP4 cache into out (as Q) and lse (float32
+    [q_rows, q_heads], or None).
+
+    kv_len int32 [batch]; page_table int32 [batch, pages_per_seq], or None: the sequences' slots in order, of
+    pages_per_seq * page_size each (by default an equal share of the cache).  q_start int32 [batch + 1] (max_q bounds
+    its differences, by default all rows), or None: max_q rows each (by default an equal share).  scale defaults to
+    head_dim ** -0.5.  workspace (uint8, kq_attention_mx_workspace bytes) is allocated for the call if None."""
+    rows, width = Q.shape
+    batch = kv_len.shape[0]
+    dim = width // q_heads
+    if width != q_heads * dim:
+        raise ValueError(f"Q: {width} columns are not {q_heads} heads")
+    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, kv_heads * dim)
+    if page_table is not None:
+        pages_per_seq = page_table.shape[1]
+        if page_size is None:
+            raise ValueError("page_size is needed with a page_table")
+    elif page_size is None:
+        page_size, pages_per_seq = max(1, n // max(1, batch)), 1
+    elif pages_per_seq is None:
+        pages_per_seq = n // page_size // max(1, batch)
+    if max_q is None:
+        max_q = rows // max(1, batch) if q_start is None else rows
+    dev = _one_device(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, page_table, q_start, lse, workspace)
+    q, qs = _rows(Q, "Q", width, rows)
+    o, os_ = _rows(out, "out", width, rows)
+    need = kq_attention_mx_workspace(rows, batch, max_q, q_heads, kv_heads, dim, pages_per_seq * page_size)
+    if workspace is None and need:
+        if stream is None:
+            with torch.cuda.device(dev):
+                workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        else:  # memory of the stream that uses it, so that its reuse waits for this call
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
+            with torch.cuda.stream(s):
+                workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+    wbytes = 0 if workspace is None else workspace.numel()
+    _call(lib().kq_attention_mx, "kq_attention_mx", dev, stream, q, qs, rows,
+          _full(q_start, "q_start", _I32, (batch + 1,)), batch, max_q, *pools, n,
+          _full(page_table, "page_table", _I32, (batch, pages_per_seq)), pages_per_seq, page_size,
+          _full(kv_len, "kv_len", _I32, (batch,)), q_heads, kv_heads, dim, dim ** -0.5 if scale is None else scale,
+          int(causal), o, os_, _full(lse, "lse", _F32, (rows, q_heads)),
+          _full(workspace, "workspace", _U8, (wbytes,)), wbytes)
+    return out, lse

@@ -26,7 +26,8 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 
-SOURCES = ["kq_api.hip", "kq_mfma.hip", "kq_quad.hip", "kq_flat.hip", "kq_build.hip", "kq_stats.hip", "kq_gemm.hip"]
+SOURCES = ["kq_api.hip", "kq_mfma.hip", "kq_quad.hip", "kq_flat.hip", "kq_build.hip", "kq_stats.hip", "kq_gemm.hip",
+           "kq_gemm_rows.hip", "kq_cache.hip", "kq_attn.hip"]
 
 
 def _compile(src: str) -> str:

@@ -287,6 +287,115 @@ kq_status build_blocks(const float* K_params, int64_t nb, float* K_f32, uint16_t
   return from_hip(kq::launch_build(K_params, (int)nb, K_f32, K_bf16, K_bf16 ? n_split : 0, inverse_t, stream));
 }
 
+// Bytes from the first to the last element of `rows` rows of `width` bf16 at `stride`.
+uint64_t strided_bytes(int64_t rows, int64_t stride, int64_t width) {
+  return rows > 0 ? (uint64_t)((rows - 1) * stride + width) * 2 : 0;
+}
+
+// Row strides of bf16 matrices read and written 16 bytes at a time; bounded so that no offset overflows.
+bool good_stride(int64_t stride, int64_t width) {
+  return stride >= width && stride % 8 == 0 && stride <= (int64_t(1) << 31);
+}
+
+// Whether two row sets of the same count and width, at the same stride, interleave without touching (column
+// ranges of one matrix).
+bool columns_apart(const uint16_t* x, const uint16_t* y, int64_t stride, int64_t width) {
+  int64_t d = (int64_t)((reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) / 2) % stride;
+  if (d < 0) d += stride;
+  return d >= width && d + width <= stride;
+}
+
+// Shared body of kq_cache_write and kq_cache_read.  k / v: the rows, read (write) or written (read).
+kq_status run_cache(bool write, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                    int64_t tokens, int64_t width, const int32_t* slots, int64_t n_slots, const uint8_t* kc,
+                    const uint8_t* ks, const uint8_t* vc, const uint8_t* vs, hipStream_t stream) {
+  const kq_status st = check_shape(tokens, width);
+  if (st != KQ_OK) return st;
+  if (n_slots < 0 || n_slots >= (int64_t(1) << 31)) return KQ_ERR_SHAPE;
+  if (!good_stride(k_stride, width) || (v && !good_stride(v_stride, width))) return KQ_ERR_SHAPE;
+  if (tokens == 0) return KQ_OK;
+  if (!k || !slots || !kc || !ks || (v && (!vc || !vs))) return KQ_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(kc, 16) || !aligned(ks, 4) || !aligned(slots, 4)) return KQ_ERR_ALIGN;
+  if (v && (!aligned(v, 16) || !aligned(vc, 16) || !aligned(vs, 4))) return KQ_ERR_ALIGN;
+  const uint64_t nc = (uint64_t)n_slots * (uint64_t)width / 2, ns = nc / 16;
+  const Range rows[] = {{k, strided_bytes(tokens, k_stride, width)}, {v, v ? strided_bytes(tokens, v_stride, width) : 0}};
+  const Range pools[] = {{kc, nc}, {ks, ns}, {v ? vc : nullptr, nc}, {v ? vs : nullptr, ns}};
+  const Range table[] = {{slots, (uint64_t)tokens * 4}};
+  if (write) {
+    if (any_alias(pools, 4, rows, 2) || any_alias(pools, 4, table, 1)) return KQ_ERR_ALIAS;
+  } else {
+    for (const Range& r : rows)
+      if (any_alias(&r, 1, pools, 4) || any_alias(&r, 1, table, 1)) return KQ_ERR_ALIAS;
+    // the two outputs may be column ranges of one matrix
+    if (overlap(rows[0], rows[1]) && !(k_stride == v_stride && columns_apart(k, v, k_stride, width)))
+      return KQ_ERR_ALIAS;
+  }
+  if (write && n_slots == 0) return KQ_OK;
+  kq::CacheArgs a{};
+  a.k = k;
+  a.v = v;
+  a.k_out = const_cast<uint16_t*>(k);
+  a.v_out = const_cast<uint16_t*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.slots = slots;
+  a.tokens = tokens;
+  a.n_slots = (int)n_slots;
+  a.chunks = (int)(width / 8);
+  a.k_codes = const_cast<uint8_t*>(kc);
+  a.k_scales = const_cast<uint8_t*>(ks);
+  a.v_codes = const_cast<uint8_t*>(vc);
+  a.v_scales = const_cast<uint8_t*>(vs);
+  return from_hip(kq::launch_cache(write, v != nullptr, a, stream));
+}
+
+// Rows up to which kq_gemm_mx_ex takes the few-row form.
+constexpr int64_t kFewRows = 64;
+
+// Shared body of kq_gemm_mx (no epilogue) and kq_gemm_mx_ex.
+kq_status run_gemm(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, const uint8_t* B_codes,
+                   const uint8_t* B_scales, int64_t N, int64_t K, kq::Epilogue e, int64_t rows_per_sample,
+                   float* Y_f32, uint16_t* Y_bf16, hipStream_t stream) {
+  if (M < 0 || N < 0 || K <= 0 || K % 32 != 0) return KQ_ERR_SHAPE;
+  if (M > (int64_t(1) << 23) || N > (int64_t(1) << 22) || K > (int64_t(1) << 24)) return KQ_ERR_SHAPE;
+  if (M == 0 || N == 0) return KQ_OK;
+  if (!A_codes || !A_scales || !B_codes || !B_scales || (!Y_f32 && !Y_bf16)) return KQ_ERR_NULL;
+  if (!aligned(A_codes, 16) || !aligned(B_codes, 16) || (Y_f32 && !aligned(Y_f32, 4)) ||
+      (Y_bf16 && !aligned(Y_bf16, 2)) || !aligned(e.bias, 4) || !aligned(e.gate, 4) || !aligned(e.residual, 2))
+    return KQ_ERR_ALIGN;
+  const uint64_t mk = (uint64_t)M * (uint64_t)K, nk = (uint64_t)N * (uint64_t)K, mn = (uint64_t)M * (uint64_t)N;
+  const Range outs[] = {{Y_f32, Y_f32 ? mn * 4 : 0}, {Y_bf16, Y_bf16 ? mn * 2 : 0}};
+  // rows of a sample: at least M is one sample
+  if (e.gate) e.by_rows = kq::make_divisor((unsigned)std::min(rows_per_sample, M));
+  const uint64_t samples = e.gate ? (uint64_t)((M + rows_per_sample - 1) / rows_per_sample) : 0;
+  const bool in_place = e.residual && e.residual == Y_bf16;  // each element is read before it is written, by one lane
+  const Range ins[] = {{A_codes, mk / 2},
+                       {A_scales, mk / 32},
+                       {B_codes, nk / 2},
+                       {B_scales, nk / 32},
+                       {e.bias, (uint64_t)N * 4},
+                       {e.gate, samples * (uint64_t)N * 4},
+                       {in_place ? nullptr : e.residual, mn * 2}};
+  if (any_alias(outs, 2, ins, 7)) return KQ_ERR_ALIAS;
+  kq::GemmArgs g{A_codes, A_scales, B_codes, B_scales, (int)M, (int)N, (int)K, Y_f32, Y_bf16, e};
+  // K = 32: a row has one scale byte, and the tile kernel's 4-byte scale reads of the last rows but one would
+  // cross the end of the tensor (kq_gemm.hip patches the last row only, which is enough from K = 64 on)
+  if (K == 32 || (e.on && M <= kFewRows)) return from_hip(kq::launch_gemm_rows(g, stream));
+  return from_hip(kq::launch_gemm(g, stream));
+}
+
+// Sizes of kq_attention_mx that do not depend on its buffers.
+kq_status check_attention(int64_t q_rows, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
+                          int64_t head_dim, int64_t capacity) {
+  const int64_t most = int64_t(1) << 30;
+  if (q_rows < 0 || q_rows >= (int64_t(1) << 28) || batch < 0 || batch > 65535 || max_q < 0 || max_q > q_rows)
+    return KQ_ERR_SHAPE;
+  if (kv_heads <= 0 || q_heads <= 0 || q_heads > 65535 || q_heads % kv_heads != 0) return KQ_ERR_SHAPE;
+  if (head_dim <= 0 || head_dim > 128 || head_dim % 8 != 0 || kv_heads * head_dim % 32 != 0) return KQ_ERR_SHAPE;
+  if (capacity < 0 || capacity > most || max_q * q_heads > most || batch * max_q * q_heads > most) return KQ_ERR_SHAPE;
+  return KQ_OK;
+}
+
 }  // namespace
 
 namespace kq {
@@ -354,6 +463,7 @@ const char* kq_status_str(kq_status s) {
     case KQ_ERR_VARIANT: return "invalid variant or missing variant input";
     case KQ_ERR_HIP: return "HIP launch failure";
     case KQ_ERR_ALIAS: return "output overlaps an input or another output";
+    case KQ_ERR_WORKSPACE: return "workspace missing or too small";
   }
   return "unknown status";
 }
@@ -479,22 +589,112 @@ kq_status kq_stream_probe(const uint16_t* X, int64_t tokens, int64_t d, uint8_t*
   return from_hip(kq::launch_flat(kq::FRONT_PROBE, false, a, stream));
 }
 
+kq_status kq_cache_write(const uint16_t* K, int64_t K_stride, const uint16_t* V, int64_t V_stride, int64_t tokens,
+                         int64_t width, const int32_t* slots, int64_t n_slots, uint8_t* K_codes, uint8_t* K_scales,
+                         uint8_t* V_codes, uint8_t* V_scales, hipStream_t stream) {
+  return run_cache(true, K, K_stride, V, V_stride, tokens, width, slots, n_slots, K_codes, K_scales, V_codes, V_scales,
+                   stream);
+}
+
+kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const uint8_t* V_codes,
+                        const uint8_t* V_scales, int64_t n_slots, int64_t width, const int32_t* slots, int64_t tokens,
+                        uint16_t* K, int64_t K_stride, uint16_t* V, int64_t V_stride, hipStream_t stream) {
+  return run_cache(false, K, K_stride, V, V_stride, tokens, width, slots, n_slots, K_codes, K_scales, V_codes,
+                   V_scales, stream);
+}
+
+int64_t kq_attention_mx_workspace(int64_t q_rows, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
+                                  int64_t head_dim, int64_t capacity) {
+  if (check_attention(q_rows, batch, max_q, q_heads, kv_heads, head_dim, capacity) != KQ_OK) return 0;
+  return kq::attn_workspace(q_rows, q_heads, head_dim, kq::attn_splits(batch, max_q, q_heads, kv_heads, capacity));
+}
+
+kq_status kq_attention_mx(const uint16_t* Q, int64_t Q_stride, int64_t q_rows, const int32_t* q_start, int64_t batch,
+                          int64_t max_q, const uint8_t* K_codes, const uint8_t* K_scales, const uint8_t* V_codes,
+                          const uint8_t* V_scales, int64_t n_slots, const int32_t* page_table, int64_t pages_per_seq,
+                          int64_t page_size, const int32_t* kv_len, int64_t q_heads, int64_t kv_heads,
+                          int64_t head_dim, float scale, int causal, uint16_t* out, int64_t out_stride, float* lse,
+                          void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (page_size <= 0 || page_size > (int64_t(1) << 24) || pages_per_seq < 0 || pages_per_seq > (int64_t(1) << 30))
+    return KQ_ERR_SHAPE;
+  const int64_t capacity = pages_per_seq * page_size;
+  const kq_status st = check_attention(q_rows, batch, max_q, q_heads, kv_heads, head_dim, capacity);
+  if (st != KQ_OK) return st;
+  if (n_slots < 0 || n_slots >= (int64_t(1) << 31)) return KQ_ERR_SHAPE;
+  if (!page_table && batch * capacity > n_slots) return KQ_ERR_SHAPE;
+  if (!q_start && batch * max_q > q_rows) return KQ_ERR_SHAPE;
+  const int64_t q_width = q_heads * head_dim;
+  if (!good_stride(Q_stride, q_width) || !good_stride(out_stride, q_width)) return KQ_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 3.0e38f) return KQ_ERR_SHAPE;
+  if (batch == 0 || max_q == 0) return KQ_OK;
+  if (!Q || !K_codes || !K_scales || !V_codes || !V_scales || !kv_len || !out) return KQ_ERR_NULL;
+  if (!aligned(Q, 16) || !aligned(out, 16) || !aligned(K_codes, 16) || !aligned(V_codes, 16) || !aligned(K_scales, 4) ||
+      !aligned(V_scales, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(page_table, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, 16))
+    return KQ_ERR_ALIGN;
+  const int nsplits = kq::attn_splits(batch, max_q, q_heads, kv_heads, capacity);
+  const int64_t need = kq::attn_workspace(q_rows, q_heads, head_dim, nsplits);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return KQ_ERR_WORKSPACE;
+  const uint64_t nc = (uint64_t)n_slots * (uint64_t)(kv_heads * head_dim) / 2;
+  const Range outs[] = {{out, strided_bytes(q_rows, out_stride, q_width)},
+                        {lse, (uint64_t)q_rows * (uint64_t)q_heads * 4},
+                        {need > 0 ? workspace : nullptr, (uint64_t)need}};
+  const Range ins[] = {{Q, strided_bytes(q_rows, Q_stride, q_width)},
+                       {K_codes, nc},
+                       {K_scales, nc / 16},
+                       {V_codes, nc},
+                       {V_scales, nc / 16},
+                       {kv_len, (uint64_t)batch * 4},
+                       {q_start, (uint64_t)(batch + 1) * 4},
+                       {page_table, (uint64_t)(batch * pages_per_seq) * 4}};
+  if (any_alias(outs, 3, ins, 8)) return KQ_ERR_ALIAS;
+  kq::AttnArgs a{};
+  a.q = Q;
+  a.q_stride = Q_stride;
+  a.q_rows = q_rows;
+  a.q_start = q_start;
+  a.batch = (int)batch;
+  a.max_q = (int)max_q;
+  a.k_codes = K_codes;
+  a.k_scales = K_scales;
+  a.v_codes = V_codes;
+  a.v_scales = V_scales;
+  a.n_pages = (int)(n_slots / page_size);
+  a.table = page_table;
+  a.pages_per_seq = (int)pages_per_seq;
+  a.page_size = (int)page_size;
+  a.kv_len = kv_len;
+  a.q_heads = (int)q_heads;
+  a.kv_heads = (int)kv_heads;
+  a.head_dim = (int)head_dim;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.lse = lse;
+  a.part = static_cast<float*>(workspace);
+  return from_hip(kq::launch_attn(a, nsplits, stream));
+}
+
 kq_status kq_gemm_mx(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, const uint8_t* B_codes,
                      const uint8_t* B_scales, int64_t N, int64_t K, float* Y_f32, uint16_t* Y_bf16,
                      hipStream_t stream) {
-  if (M < 0 || N < 0 || K <= 0 || K % 32 != 0) return KQ_ERR_SHAPE;
-  if (M > (int64_t(1) << 23) || N > (int64_t(1) << 22) || K > (int64_t(1) << 24)) return KQ_ERR_SHAPE;
-  if (M == 0 || N == 0) return KQ_OK;
-  if (!A_codes || !A_scales || !B_codes || !B_scales || (!Y_f32 && !Y_bf16)) return KQ_ERR_NULL;
-  if (!aligned(A_codes, 16) || !aligned(B_codes, 16) || (Y_f32 && !aligned(Y_f32, 4)) ||
-      (Y_bf16 && !aligned(Y_bf16, 2)))
-    return KQ_ERR_ALIGN;
-  const uint64_t mk = (uint64_t)M * (uint64_t)K, nk = (uint64_t)N * (uint64_t)K, mn = (uint64_t)M * (uint64_t)N;
-  const Range outs[] = {{Y_f32, Y_f32 ? mn * 4 : 0}, {Y_bf16, Y_bf16 ? mn * 2 : 0}};
-  const Range ins[] = {{A_codes, mk / 2}, {A_scales, mk / 32}, {B_codes, nk / 2}, {B_scales, nk / 32}};
-  if (any_alias(outs, 2, ins, 4)) return KQ_ERR_ALIAS;
-  kq::GemmArgs g{A_codes, A_scales, B_codes, B_scales, (int)M, (int)N, (int)K, Y_f32, Y_bf16};
-  return from_hip(kq::launch_gemm(g, stream));
+  return run_gemm(A_codes, A_scales, M, B_codes, B_scales, N, K, kq::Epilogue{}, 0, Y_f32, Y_bf16, stream);
+}
+
+kq_status kq_gemm_mx_ex(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, const uint8_t* B_codes,
+                        const uint8_t* B_scales, int64_t N, int64_t K, const float* bias, kq_act act,
+                        const float* gate, int64_t rows_per_sample, const uint16_t* residual, float* Y_f32,
+                        uint16_t* Y_bf16, hipStream_t stream) {
+  if ((int)act < KQ_ACT_NONE || (int)act > KQ_ACT_SILU) return KQ_ERR_VARIANT;
+  if (gate && rows_per_sample <= 0) return KQ_ERR_SHAPE;
+  kq::Epilogue e{};
+  e.on = true;
+  e.act = (int)act;
+  e.bias = bias;
+  e.gate = gate;
+  e.residual = residual;
+  return run_gemm(A_codes, A_scales, M, B_codes, B_scales, N, K, e, gate ? rows_per_sample : 0, Y_f32, Y_bf16, stream);
 }
 
 kq_status kq_tune(const uint16_t* X, int64_t tokens, int64_t d, const float* K_params, const uint16_t* K_bf16,

@@ -27,7 +27,11 @@
 // fragment read touches at a fixed chunk fall on distinct banks.  Rows past
 // M or N and K blocks past K load as zero codes (buffer range /
 // out-of-range offsets), which add nothing.
+//
+// kq_gemm_mx_ex is the same kernel with an epilogue on the fp32 sums (EPI):
+// bias, activation, per-sample gate and residual before the one rounding.
 #include "kq_device.hpp"
+#include "kq_epilogue.hpp"
 #include "kq_internal.h"
 
 namespace kq {
@@ -93,7 +97,7 @@ __device__ __forceinline__ void lds_barrier() {
 // One output tile of 64 MI rows x 256 columns at (m0, n0): MI = 4 is the
 // whole 256 x 256 tile, MI = 2 half of one (see launch_gemm).  Each wave
 // computes 32 MI rows x 64 columns (MI x 2 MFMA tiles of 32 x 32).
-template <int MI>
+template <int MI, bool EPI>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uint8_t (&a_st)[kStages][kTileB],
                                           uint8_t (&b_st)[kStages][kTileB], uint8_t (&as_st)[2][kScB],
                                           uint8_t (&bs_st)[2][kScB]) {
@@ -308,6 +312,31 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
     const int band = 32 * MI * wm + 32 * i;
     const int brows = min(32, max(0, mrows - band));
     const int64_t base = (int64_t)(m0 + band) * N;
+    if constexpr (EPI) {
+      const auto rr = rsrc_uniform(g.epi.residual ? g.epi.residual + base : nullptr,
+                                   g.epi.residual ? (int64_t)brows * N * 2 : 0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = 64 * wn + 32 * j + fr;
+        const bool in = col < nrows;
+        float res[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = 8 * (r >> 2) + 4 * fh + (r & 3);
+          const unsigned short w =
+              __builtin_amdgcn_raw_buffer_load_b16(rr, in ? (uint32_t)((row * N + n0 + col) * 2) : kOut, 0, 0);
+          res[r] = bf16_lo(w);
+        }
+        float v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
+        epilogue<16>(g.epi, v, res, in ? n0 + col : 0, g.N, [&](int r) {
+          return min(m0 + band + 8 * (r >> 2) + 4 * fh + (r & 3), g.M - 1);
+        });
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = v[r];
+      }
+    }
     if (g.y_f32) {
       const auto ry = rsrc_uniform(g.y_f32 + base, (int64_t)brows * N * 4);
 #pragma unroll
@@ -346,6 +375,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
 // are dealt to them in turn) so that XCD x takes the x-th eighth of its
 // range of the order, and the workgroups running at once on one XCD share A
 // rows and B rows in its L2.
+template <bool EPI>
 __global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t a_st[kStages][kTileB];
   __shared__ __attribute__((aligned(1024))) uint8_t b_st[kStages][kTileB];
@@ -370,27 +400,28 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
   const int w = t - grp * per_group;
   const int tm = first + w % rows, tn = w / rows;
   if (whole)
-    gemm_tile<4>(g, tm * kBM, tn * kBN, a_st, b_st, as_st, bs_st);
+    gemm_tile<4, EPI>(g, tm * kBM, tn * kBN, a_st, b_st, as_st, bs_st);
   else
-    gemm_tile<2>(g, tm * kBM + 128 * half, tn * kBN, a_st, b_st, as_st, bs_st);
+    gemm_tile<2, EPI>(g, tm * kBM + 128 * half, tn * kBN, a_st, b_st, as_st, bs_st);
 }
 
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& args, hipStream_t stream) {
   GemmArgs g = args;
+  const void* fn = g.epi.on ? (const void*)&gemm_kernel<true> : (const void*)&gemm_kernel<false>;
   // Wave quantisation: with `slots` workgroups resident at once, the tiles
   // past the last whole multiple of `slots` run as a partial last round.
   // When that round fills at most half the slots, its tiles are computed as
   // two halves each (twice the workgroups, each half the work).
   const int64_t tiles = (int64_t)((g.N + kBN - 1) / kBN) * ((g.M + kBM - 1) / kBM);
-  const int64_t slots = (int64_t)cu_count() * resident_per_cu((const void*)&gemm_kernel, kThreads);
+  const int64_t slots = (int64_t)cu_count() * resident_per_cu(fn, kThreads);
   const int64_t rem = tiles % slots;
   const bool split = rem > 0 && 2 * rem <= slots && (tiles - rem) % 8 == 0;
   g.full_tiles = (int)(split ? tiles - rem : tiles);
   const dim3 grid((unsigned)(split ? tiles + rem : tiles));
   void* kargs[] = {&g};
-  return hipLaunchKernel((const void*)&gemm_kernel, grid, dim3(kThreads), kargs, 0, stream);
+  return hipLaunchKernel(fn, grid, dim3(kThreads), kargs, 0, stream);
 }
 
 }  // namespace kq

@@ -99,6 +99,28 @@ int chunks_one_round(const void* fn, int block_threads, int ngroups, int ntiles,
 hipError_t launch_mfma(int ksrc, bool store_y, bool mod, const MfmaArgs& args, hipStream_t stream);
 hipError_t launch_quad(int front, bool store_y, const QuadArgs& args, hipStream_t stream);
 hipError_t launch_flat(int front, bool store_y, const FlatArgs& args, hipStream_t stream);
+// Division of 31-bit numbers by a run-time constant (kq_mxval.hpp, fast_div).
+struct Divisor {
+  uint32_t m;
+  int shift;
+};
+
+inline Divisor make_divisor(unsigned d) {
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  return Divisor{(uint32_t)(((uint64_t)1 << (31 + l)) / d + 1), 31 + l};  // m <= 2^32 - 2^8 for d <= 2^24
+}
+
+// What kq_gemm_mx_ex does to each fp32 sum: (residual + gate[sample] * act(sum + bias)); null: left out.
+struct Epilogue {
+  bool on = false;  // any of it
+  int act = 0;      // kq_act
+  const float* bias = nullptr;
+  const float* gate = nullptr;  // [samples][N]
+  Divisor by_rows{};            // rows of a sample
+  const uint16_t* residual = nullptr;
+};
+
 // W4A4 GEMM: Y [M][N] = deq(A) deq(B)^T, A [M][K] and B [N][K] in MXFP4
 // (codes [rows][K/2], E8M0 scales [rows][K/32]); either output may be null.
 struct GemmArgs {
@@ -109,10 +131,65 @@ struct GemmArgs {
   int M, N, K;
   float* y_f32;
   uint16_t* y_bf16;
+  Epilogue epi;
   int full_tiles;  // set by launch_gemm: tiles computed whole; the rest in two halves
 };
 
+// MXFP4 key/value cache, write or read: rows of 8 * chunks channels, slots
+// [tokens], pools of n_slots rows.  Strides in elements.
+struct CacheArgs {
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int64_t k_stride, v_stride;
+  const int32_t* slots;
+  int64_t tokens;
+  int n_slots;
+  int chunks;
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  Divisor by_chunks;  // set by launch_cache
+};
+
+// Attention over the cache: see kq_attn.hip.  Strides in elements.
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_stride, q_rows;
+  const int32_t* q_start;  // [batch + 1], or null: max_q rows per sequence
+  int batch, max_q;
+  const uint8_t* k_codes;
+  const uint8_t* k_scales;
+  const uint8_t* v_codes;
+  const uint8_t* v_scales;
+  int n_pages;
+  const int32_t* table;  // [batch][pages_per_seq], or null: pages in order
+  int pages_per_seq, page_size;
+  const int32_t* kv_len;
+  int q_heads, kv_heads, head_dim;
+  float scale;
+  int causal;
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;
+  float* part;  // workspace of a split launch
+  // set by the launch
+  Divisor by_page, by_group;
+  int capacity, group, row_tiles, nsplits;
+  float c;  // scale * log2(e)
+};
+
+// Key ranges the launch divides each sequence into (1: no workspace), and the workspace bytes that takes.
+int attn_splits(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t capacity);
+int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, int nsplits);
+hipError_t launch_attn(const AttnArgs& args, int nsplits, hipStream_t stream);
+
+hipError_t launch_cache(bool write, bool both, const CacheArgs& args, hipStream_t stream);
 hipError_t launch_gemm(const GemmArgs& args, hipStream_t stream);
+// The same for few rows, or K = 32 (kq_gemm_rows.hip).
+hipError_t launch_gemm_rows(const GemmArgs& args, hipStream_t stream);
 hipError_t launch_row_stats(const uint16_t* X, int T, int d, double eps, float* stats, hipStream_t stream);
 hipError_t launch_build(const float* P, int nb, float* K32, uint16_t* Kbf, int n_split, int inverse_t,
                         hipStream_t stream);
