@@ -94,6 +94,92 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The epilogue's output: a wave's 32 MI x 64 tile, a band of 32 rows at a
+// time through a wave-private piece of the ring (free after the last stage),
+// so that a lane holds eight consecutive channels of a row.  Bias, gate,
+// residual and output are then 16-byte accesses, eight whole 128-byte rows an
+// instruction; and the lane's channels are the same for every row.  (With a
+// value's row and channel as the matrix cores leave them, residual and output
+// are 2-byte accesses, 256 of them per lane; their addresses beside the
+// accumulators spilled 52 registers, and the 8192 x 4608 x 1152 product with
+// bias and GELU took 90 us.)  Residual rows are loaded a band ahead, and the
+// gate is kept in registers where the wave's rows are of one sample: with
+// bias, gate and residual that product went from 98 to 73 us (the product
+// alone: 48).  Non-temporal stores: 2-7% faster than device scope or the default here.
+constexpr int kBandStride = 68;               // floats per row of a band: 64 and a pad against bank conflicts
+constexpr int kBandF = 32 * kBandStride;      // floats per wave
+static_assert(8 * kBandF * 4 <= kStages * kTileB * 2, "the bands fit the ring");
+
+template <int MI>
+__device__ __forceinline__ void store_epilogue(const GemmArgs& g, const f32x16 (&acc)[MI][2], int m0, int n0,
+                                               int mrows, int wm, int wn, int lane, float* band) {
+  const int fr = lane & 31, fh = lane >> 5;
+  const int n = n0 + 64 * wn + 8 * (lane & 7);  // the lane's channels n .. n + 7
+  const int cols = max(0, min(8, g.N - n));
+  const int64_t N = g.N;
+  const int base = 32 * MI * wm;  // the wave's first row of the tile
+  // 16-byte accesses where every row allows them (then the lane has all its channels or none)
+  const bool vec = (g.N & 7) == 0 &&
+                   ((reinterpret_cast<uintptr_t>(g.epi.residual) | reinterpret_cast<uintptr_t>(g.y_bf16) |
+                     reinterpret_cast<uintptr_t>(g.y_f32)) & 15) == 0;  // uniform
+  LaneColumns<8> lane_cols(g.epi, n, cols);
+  lane_cols.load_gate(g, m0 + base, min(m0 + base + 32 * MI, g.M) - 1);
+  // residual rows of a band, loaded a band ahead of their use
+  u32x4 res[2][4];
+  auto load_res = [&](int i) {
+    const int brows = min(32, max(0, mrows - base - 32 * i));
+    const auto rr = rsrc_uniform(g.epi.residual + (m0 + base + 32 * i) * N, (int64_t)brows * N * 2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 8 * k + (lane >> 3);
+      const uint32_t off = cols > 0 ? (uint32_t)((row * g.N + n) * 2) : kOut;
+      res[i & 1][k] = __builtin_amdgcn_raw_buffer_load_b128(rr, off, 0, 0);
+    }
+  };
+  const bool ahead = g.epi.residual && vec;  // uniform
+  if (ahead) load_res(0);
+  lds_barrier();  // every wave is past its last fragment read
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int r0 = base + 32 * i;  // the band's first row of the tile
+    if (ahead && i + 1 < MI) load_res(i + 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) band[(8 * (r >> 2) + 4 * fh + (r & 3)) * kBandStride + 32 * j + fr] = acc[i][j][r];
+    const int brows = min(32, max(0, mrows - r0));
+    const auto yf = rsrc_uniform(g.y_f32 + (m0 + r0) * N, vec && g.y_f32 ? (int64_t)brows * N * 4 : 0);
+    const auto yb = rsrc_uniform(g.y_bf16 + (m0 + r0) * N, vec && g.y_bf16 ? (int64_t)brows * N * 2 : 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 8 * k + (lane >> 3), m = min(m0 + r0 + row, g.M - 1);
+      const f32x4* src = reinterpret_cast<const f32x4*>(&band[row * kBandStride + 8 * (lane & 7)]);
+      const f32x4 lo = src[0], hi = src[1];
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (vec) {
+        float r8[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) r8[c] = c & 1 ? bf16_hi(res[i & 1][k][c >> 1]) : bf16_lo(res[i & 1][k][c >> 1]);
+        lane_cols.apply(g, v, m, r8);
+        const uint32_t at = (uint32_t)(row * g.N + n);
+        if (g.y_f32) {
+          const f32x4 w0 = {v[0], v[1], v[2], v[3]}, w1 = {v[4], v[5], v[6], v[7]};
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w0), yf, cols > 0 ? 4 * at : kOut, 0, kNT);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w1), yf, cols > 0 ? 4 * at + 16 : kOut, 0, kNT);
+        }
+        if (g.y_bf16) {
+          bf16x8 w;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) w[c] = (__bf16)v[c];
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), yb, cols > 0 ? 2 * at : kOut, 0, kNT);
+        }
+      } else if (row < brows) {
+        lane_cols.apply_and_store(g, v, m);
+      }
+    }
+  }
+}
+
 // One output tile of 64 MI rows x 256 columns at (m0, n0): MI = 4 is the
 // whole 256 x 256 tile, MI = 2 half of one (see launch_gemm).  Each wave
 // computes 32 MI rows x 64 columns (MI x 2 MFMA tiles of 32 x 32).
@@ -102,7 +188,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
                                           uint8_t (&b_st)[kStages][kTileB], uint8_t (&as_st)[2][kScB],
                                           uint8_t (&bs_st)[2][kScB]) {
   constexpr int BM = 64 * MI;   // rows of the tile
-  constexpr int NA = MI / 2;    // 16-row groups of A each wave stages per stage
+  constexpr int NA = (MI + 1) / 2;  // 16-row groups of A each wave stages per stage (MI = 3: four lie past the tile, no rows)
   constexpr int kOps = NA + 2;  // code loads per wave and stage
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -307,36 +393,15 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
   // stores: 1-9% faster than the default policy at the DiT shapes (MI355X), non-temporal ones
   // no faster.
   const int64_t N = g.N;
+  if constexpr (EPI) {
+    store_epilogue<MI>(g, acc, m0, n0, mrows, wm, wn, lane, reinterpret_cast<float*>(&a_st[0][0]) + wv * kBandF);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int band = 32 * MI * wm + 32 * i;
     const int brows = min(32, max(0, mrows - band));
     const int64_t base = (int64_t)(m0 + band) * N;
-    if constexpr (EPI) {
-      const auto rr = rsrc_uniform(g.epi.residual ? g.epi.residual + base : nullptr,
-                                   g.epi.residual ? (int64_t)brows * N * 2 : 0);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = 64 * wn + 32 * j + fr;
-        const bool in = col < nrows;
-        float res[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int row = 8 * (r >> 2) + 4 * fh + (r & 3);
-          const unsigned short w =
-              __builtin_amdgcn_raw_buffer_load_b16(rr, in ? (uint32_t)((row * N + n0 + col) * 2) : kOut, 0, 0);
-          res[r] = bf16_lo(w);
-        }
-        float v[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
-        epilogue<16>(g.epi, v, res, in ? n0 + col : 0, g.N, [&](int r) {
-          return min(m0 + band + 8 * (r >> 2) + 4 * fh + (r & 3), g.M - 1);
-        });
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = v[r];
-      }
-    }
     if (g.y_f32) {
       const auto ry = rsrc_uniform(g.y_f32 + base, (int64_t)brows * N * 4);
 #pragma unroll
@@ -382,7 +447,8 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
   __shared__ __attribute__((aligned(256))) uint8_t as_st[2][kScB];  // by parity of the stage group
   __shared__ __attribute__((aligned(256))) uint8_t bs_st[2][kScB];
 
-  const int gm = (g.M + kBM - 1) / kBM, gn = (g.N + kBN - 1) / kBN;
+  const int bm = EPI ? 64 * g.tile_mi : kBM;
+  const int gm = (g.M + bm - 1) / bm, gn = (g.N + kBN - 1) / kBN;
   const int b = (int)blockIdx.x;
   const bool whole = b < g.full_tiles;  // workgroup-uniform
   int t, half = 0;
@@ -399,7 +465,9 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
   const int rows = min(kGroupM, gm - first);
   const int w = t - grp * per_group;
   const int tm = first + w % rows, tn = w / rows;
-  if (whole)
+  if (EPI && g.tile_mi == 3)
+    gemm_tile<3, EPI>(g, tm * 192, tn * kBN, a_st, b_st, as_st, bs_st);
+  else if (whole)
     gemm_tile<4, EPI>(g, tm * kBM, tn * kBN, a_st, b_st, as_st, bs_st);
   else
     gemm_tile<2, EPI>(g, tm * kBM + 128 * half, tn * kBN, a_st, b_st, as_st, bs_st);
@@ -414,10 +482,18 @@ hipError_t launch_gemm(const GemmArgs& args, hipStream_t stream) {
   // past the last whole multiple of `slots` run as a partial last round.
   // When that round fills at most half the slots, its tiles are computed as
   // two halves each (twice the workgroups, each half the work).
-  const int64_t tiles = (int64_t)((g.N + kBN - 1) / kBN) * ((g.M + kBM - 1) / kBM);
   const int64_t slots = (int64_t)cu_count() * resident_per_cu(fn, kThreads);
+  const int64_t gn = (g.N + kBN - 1) / kBN;
+  // With an epilogue, a product whose 256-row tiles fill between a half and all
+  // of the GPU takes 192-row tiles where those still run in one round (4096 x
+  // 2240 x 5600: 198 tiles, 49 us, against 144 in 54 us; at half or less the
+  // tiles are halved below: 1024 x 4608 x 1152 14 us against 18).
+  const int64_t whole = gn * ((g.M + kBM - 1) / kBM);
+  g.tile_mi = g.epi.on && whole < slots && 2 * whole > slots && gn * ((g.M + 191) / 192) <= slots ? 3 : 4;
+  const int bm = 64 * g.tile_mi;
+  const int64_t tiles = gn * ((g.M + bm - 1) / bm);
   const int64_t rem = tiles % slots;
-  const bool split = rem > 0 && 2 * rem <= slots && (tiles - rem) % 8 == 0;
+  const bool split = g.tile_mi == 4 && rem > 0 && 2 * rem <= slots && (tiles - rem) % 8 == 0;
   g.full_tiles = (int)(split ? tiles - rem : tiles);
   const dim3 grid((unsigned)(split ? tiles + rem : tiles));
   void* kargs[] = {&g};

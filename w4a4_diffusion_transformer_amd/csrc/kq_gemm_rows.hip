@@ -105,18 +105,11 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(GemmArgs g) {
   for (int x = tid; x < T * T * 256; x += kThreads) {
     const int tm = x / (16 * T), tn = x % (16 * T);
     const int at = (((tm >> 4) * T + (tn >> 4)) * 4 + (tm & 3)) * 64 + ((tm & 15) >> 2) * 16 + (tn & 15);
-    float v[1] = {0.0f}, res[1] = {0.0f};
+    float v[1] = {0.0f};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v[0] += sums[w][at];
     const int m = m0 + tm, n = n0 + tn;
-    if (m >= g.M || n >= g.N) continue;
-    const int64_t to = (int64_t)m * g.N + n;
-    if (g.epi.on) {
-      if (g.epi.residual) res[0] = bf16_lo(g.epi.residual[to]);
-      epilogue<1>(g.epi, v, res, n, g.N, [&](int) { return m; });
-    }
-    if (g.y_f32) g.y_f32[to] = v[0];
-    if (g.y_bf16) g.y_bf16[to] = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
+    if (m < g.M && n < g.N) LaneColumns<1>(g.epi, n, 1).apply_and_store(g, v, m);
   }
 }
 

@@ -133,6 +133,7 @@ struct GemmArgs {
   uint16_t* y_bf16;
   Epilogue epi;
   int full_tiles;  // set by launch_gemm: tiles computed whole; the rest in two halves
+  int tile_mi;     // set by launch_gemm: rows of a tile / 64
 };
 
 // MXFP4 key/value cache, write or read: rows of 8 * chunks channels, slots
