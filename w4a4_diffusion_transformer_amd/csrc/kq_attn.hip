@@ -53,6 +53,19 @@ __device__ __forceinline__ float swap_sum32(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// Sum over the four quarters of a wave.
+__device__ __forceinline__ float quarter_sum(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return swap_sum32(__uint_as_float(s[0]) + __uint_as_float(s[1]));
+}
+
+// Orders a wave's own LDS accesses for the compiler; the hardware runs them in order.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // What one sequence and key head is to a workgroup.
 struct Seq {
   int64_t row0;  // first row of its queries in q, out and lse
@@ -326,6 +339,253 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
   store_row<NT>(a, o, m, swap_sum32(l), row, head, split, half, live);
 }
 
+// ---------------------------------------------------------------- few rows
+
+// A workgroup owns up to 16 rows; its four waves take 64-key tiles in turn,
+// each with its own loads, softmax and O, and join at the end.  What bounds
+// it is reading the cache: every code is read once, straight into registers
+// in the operand order of v_mfma_f32_16x16x32_bf16 (lane l: key l % 16 and
+// the l / 16-th quarter of the head's channels, which at head_dim 128 is one
+// MX block: one 16-byte load and one scale byte), the next tile's while this
+// one is multiplied.  Values pass through a wave-private LDS tile for their
+// transposition (32 keys at a time), so no wave waits for another.  Key order
+// within a 32-key step of the second product: index j of quarter g is key
+// 4 g + j (j < 4) or 16 + 4 g + j - 4, the order S^T has.
+// The key heads of one sequence and range follow one another on one XCD: they
+// read neighbouring parts of the same cache lines.
+constexpr int kTokenRows = 16, kTokenWaves = 4;
+
+template <int DP, bool ALIGNED>
+__global__ __launch_bounds__(64 * kTokenWaves, DP <= 64 ? 4 : 3) void attn_tokens_kernel(AttnArgs a) {
+  constexpr int NS = DP / 32, NO = DP / 16, VS = DP + 16, OS = DP + 4;
+  constexpr int kVBytes = kTokenWaves * 32 * VS * 2, kOBytes = kTokenWaves * kTokenRows * OS * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t shared[kVBytes > kOBytes ? kVBytes : kOBytes];
+  __shared__ float wave_m[kTokenWaves][kTokenRows], wave_l[kTokenWaves][kTokenRows];
+
+  const int tid = threadIdx.x, lane = tid & 63, quarter = lane >> 4, col = lane & 15;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int kvh = id % a.kv_heads;
+  id /= a.kv_heads;
+  const int tile = id % a.row_tiles;
+  id /= a.row_tiles;
+  const int split = id % a.nsplits, b = id / a.nsplits;
+  const Seq sq = sequence(a, b);
+  const int rows = min(sq.nq, a.max_q) * a.group;
+  const int r0 = tile * kTokenRows;
+  if (r0 >= rows) return;
+
+  const int last_q = (int)fast_div((unsigned)(min(r0 + kTokenRows, rows) - 1), a.by_group);
+  const int see = a.causal ? max(0, min(sq.len, sq.len - sq.nq + last_q + 1)) : sq.len;
+  const int share = ((see + a.nsplits - 1) / a.nsplits + 63) & ~63;
+  const int key0 = min(see, split * share), key1 = min(see, key0 + share);
+
+  const int r = min(r0 + col, rows - 1);
+  const int qi = (int)fast_div((unsigned)r, a.by_group);
+  const int head = kvh * a.group + (r - qi * a.group);
+  const int upto = a.causal ? sq.len - sq.nq + qi : sq.len;  // last key this lane's query sees
+  const int upto_min = __builtin_amdgcn_readfirstlane(upto);
+
+  const int nc = a.head_dim >> 3, chunk0 = kvh * nc;
+  const int64_t width8 = (int64_t)a.kv_heads * nc;
+  bf16x8 qf[NS];
+  const uint16_t* qp = a.q + (sq.row0 + qi) * a.q_stride + (int64_t)head * a.head_dim;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int ch = quarter * NS + s;
+    u32x4 w = {0, 0, 0, 0};
+    if (ch < nc) w = *reinterpret_cast<const u32x4*>(qp + 8 * ch);
+    qf[s] = __builtin_bit_cast(bf16x8, w);
+  }
+
+  // One 64-key tile of this lane: codes and scales of keys 16 k + col.
+  struct Tile {
+    unsigned kw[4][NS], vw[4][NS];
+    unsigned kb[4][ALIGNED ? 1 : NS], vb[4][ALIGNED ? 1 : NS];
+    uint64_t seen;
+  };
+  auto load = [&](int slot, Tile& t) {
+    t.seen = __builtin_amdgcn_ballot_w64(slot >= 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int sl = __shfl(slot, 16 * k + col);
+      const int64_t at = (int64_t)max(sl, 0) * width8 + chunk0 + quarter * NS;  // slot 0 is always there
+      if constexpr (ALIGNED) {
+        typedef __attribute__((ext_vector_type(NS))) unsigned words;
+        const words kw = *reinterpret_cast<const words*>(a.k_codes + 4 * at);
+        const words vw = *reinterpret_cast<const words*>(a.v_codes + 4 * at);
+        t.kb[k][0] = a.k_scales[at >> 2];
+        t.vb[k][0] = sl >= 0 ? a.v_scales[at >> 2] : 0u;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          t.kw[k][s] = kw[s];
+          t.vw[k][s] = sl >= 0 ? vw[s] : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const bool in = quarter * NS + s < nc;
+          const int64_t c = in ? at + s : 0;
+          t.kw[k][s] = in ? *reinterpret_cast<const unsigned*>(a.k_codes + 4 * c) : 0u;
+          t.kb[k][s] = in ? a.k_scales[c >> 2] : 0u;
+          t.vw[k][s] = in && sl >= 0 ? *reinterpret_cast<const unsigned*>(a.v_codes + 4 * c) : 0u;
+          t.vb[k][s] = in && sl >= 0 ? a.v_scales[c >> 2] : 0u;
+        }
+      }
+    }
+  };
+
+  f32x4 o[NO];
+#pragma unroll
+  for (int t = 0; t < NO; ++t) o[t] = f32x4{0, 0, 0, 0};
+  float m = -__builtin_inff(), l = 0.0f;
+  uint16_t* vs = reinterpret_cast<uint16_t*>(shared) + wv * 32 * VS;
+
+  auto multiply = [&](const Tile& t, int key) {
+    f32x4 s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s[k] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int d = 0; d < NS; ++d)
+        s[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_values8(t.kw[k][d], t.kb[k][ALIGNED ? 0 : d]), qf[d], s[k], 0,
+                                                       0, 0);
+    }
+    if (t.seen != ~(uint64_t)0 || upto_min < key + 63) {
+      const uint64_t mine = t.seen >> (4 * quarter);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (!((mine >> (16 * k + x)) & 1) || key + 16 * k + 4 * quarter + x > upto) s[k][x] = -__builtin_inff();
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) top = fmaxf(top, s[k][x]);
+    if (__builtin_amdgcn_ballot_w64(top > m) != 0) {  // some query has a new maximum
+      const unsigned u = __float_as_uint(top);
+      const auto h = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+      const float mn = fmaxf(m, swap_max32(fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]))));
+      const float alpha = mn > m ? __builtin_amdgcn_exp2f((m - mn) * a.c) : 1.0f;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < NO; ++d) o[d] *= alpha;
+      m = mn;
+    }
+    const float base = m == -__builtin_inff() ? 0.0f : m * a.c;
+    bf16x8 p[2];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][x], a.c, -base));
+        sum += e;
+        p[k >> 1][4 * (k & 1) + x] = (__bf16)e;
+      }
+    l += sum;
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int d = 0; d < NS; ++d)
+          *reinterpret_cast<bf16x8*>(&vs[(16 * k + col) * VS + 8 * (quarter * NS + d)]) =
+              mx_values8(t.vw[2 * half + k][d], t.vb[2 * half + k][ALIGNED ? 0 : d]);
+      wave_lds_fence();
+      const uint16_t* at = vs + (4 * quarter + (col >> 2)) * VS + 4 * (col & 3);
+#pragma unroll
+      for (int d = 0; d < NO; ++d) {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 16 * d));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 16 * VS + 16 * d));
+        const bf16x8 w = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, p[half], o[d], 0, 0, 0);
+      }
+      wave_lds_fence();
+    }
+  };
+
+  // tiles wv, wv + 4, ... of the range: the next tile's codes are in flight during this one's
+  // product, and the slots of the one after
+  constexpr int kStep = 64 * kTokenWaves;
+  int key = key0 + 64 * wv;
+  if (key < key1) {
+    Tile cur, next;
+    load(slot_of(a, b, key + lane, key1), cur);
+    int slot = slot_of(a, b, key + kStep + lane, key1);
+    for (; key + kStep < key1; key += kStep) {
+      load(slot, next);
+      slot = slot_of(a, b, key + 2 * kStep + lane, key1);
+      multiply(cur, key);
+      cur = next;
+    }
+    multiply(cur, key);
+  }
+
+  // join the waves
+  l = quarter_sum(l);
+  if (quarter == 0) {
+    wave_m[wv][col] = m;
+    wave_l[wv][col] = l;
+  }
+  __syncthreads();  // also: every wave is done with its tile of values
+  float top = wave_m[0][col];
+#pragma unroll
+  for (int w = 1; w < kTokenWaves; ++w) top = fmaxf(top, wave_m[w][col]);
+  const float mine = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m - top) * a.c);
+  float* os = reinterpret_cast<float*>(shared);
+#pragma unroll
+  for (int d = 0; d < NO; ++d)
+    *reinterpret_cast<f32x4*>(&os[(wv * kTokenRows + col) * OS + 16 * d + 4 * quarter]) = o[d] * mine;
+  __syncthreads();
+  for (int x = tid; x < kTokenRows * nc; x += 64 * kTokenWaves) {
+    const int q = x / nc, ch = x - q * nc;
+    if (r0 + q >= rows) break;
+    float best = wave_m[0][q];
+#pragma unroll
+    for (int w = 1; w < kTokenWaves; ++w) best = fmaxf(best, wave_m[w][q]);
+    float sum = 0.0f;
+    f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kTokenWaves; ++w) {
+      sum += wave_m[w][q] == -__builtin_inff() ? 0.0f
+                                               : wave_l[w][q] * __builtin_amdgcn_exp2f((wave_m[w][q] - best) * a.c);
+      const f32x4* src = reinterpret_cast<const f32x4*>(&os[(w * kTokenRows + q) * OS + 8 * ch]);
+      lo += src[0];
+      hi += src[1];
+    }
+    const int qx = (int)fast_div((unsigned)(r0 + q), a.by_group);
+    const int h = kvh * a.group + (r0 + q - qx * a.group);
+    const int64_t row = sq.row0 + qx;
+    const float base = best == -__builtin_inff() ? best : best * a.c;
+    if (a.nsplits > 1) {
+      const int64_t n = a.q_rows * a.q_heads, at = split * n + row * a.q_heads + h;
+      if (ch == 0) {
+        float* ml = a.part + (int64_t)a.nsplits * n * a.head_dim + 2 * at;
+        ml[0] = base;
+        ml[1] = sum;
+      }
+      f32x4* dst = reinterpret_cast<f32x4*>(a.part + at * a.head_dim + 8 * ch);
+      dst[0] = lo;
+      dst[1] = hi;
+    } else {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (a.lse && ch == 0) a.lse[row * a.q_heads + h] = kLn2 * (base + __builtin_amdgcn_logf(sum));
+      bf16x8 w;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        w[c] = (__bf16)(lo[c] * inv);
+        w[4 + c] = (__bf16)(hi[c] * inv);
+      }
+      *reinterpret_cast<u32x4*>(a.out + row * a.out_stride + (int64_t)h * a.head_dim + 8 * ch) =
+          __builtin_bit_cast(u32x4, w);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- joining
 
 // One lane per eight channels of a row: the splits' outputs weighted by
@@ -375,30 +635,51 @@ const void* rows_kernel(int d) {
                    : (const void*)&attn_rows_kernel<128>;
 }
 
+const void* tokens_kernel(int d) {
+  if (d == 32) return (const void*)&attn_tokens_kernel<32, true>;
+  if (d == 64) return (const void*)&attn_tokens_kernel<64, true>;
+  if (d == 128) return (const void*)&attn_tokens_kernel<128, true>;
+  return d < 32   ? (const void*)&attn_tokens_kernel<32, false>
+         : d < 64 ? (const void*)&attn_tokens_kernel<64, false>
+         : d <= 96 ? (const void*)&attn_tokens_kernel<96, false>
+                   : (const void*)&attn_tokens_kernel<128, false>;
+}
+
 }  // namespace
 
-int attn_splits(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t capacity) {
-  const int64_t tiles = batch * kv_heads * ((max_q * (q_heads / kv_heads) + kRowsTile - 1) / kRowsTile);
-  const int64_t want = tiles > 0 ? 512 / tiles : 1, most = capacity / 128;
-  return (int)std::max<int64_t>(1, std::min(want, most));
+// Few rows: up to two 16-row tiles for each sequence and key head.
+AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t capacity) {
+  AttnPlan p;
+  const int64_t rows = max_q * (q_heads / kv_heads);
+  p.few = rows <= 2 * kTokenRows;
+  const int tile = p.few ? kTokenRows : kRowsTile;
+  p.row_tiles = (int)((rows + tile - 1) / tile);
+  const int64_t tiles = std::max<int64_t>(1, batch * kv_heads * p.row_tiles);
+  const int64_t want = (p.few ? 2048 : 512) / tiles, most = capacity / (p.few ? 256 : 128);
+  p.nsplits = (int)std::max<int64_t>(1, std::min(want, most));
+  return p;
 }
 
 int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, int nsplits) {
   return nsplits > 1 ? nsplits * q_rows * q_heads * (head_dim + 2) * 4 : 0;
 }
 
-hipError_t launch_attn(const AttnArgs& args, int nsplits, hipStream_t stream) {
+hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   AttnArgs a = args;
   a.group = a.q_heads / a.kv_heads;
   a.by_page = make_divisor((unsigned)a.page_size);
   a.by_group = make_divisor((unsigned)a.group);
   a.capacity = a.n_pages > 0 ? a.pages_per_seq * a.page_size : 0;
   a.c = a.scale * kLog2e;
-  a.nsplits = nsplits;
-  a.row_tiles = (int)(((int64_t)a.max_q * a.group + kRowsTile - 1) / kRowsTile);
+  const AttnPlan p =
+      attn_plan(a.batch, a.max_q, a.q_heads, a.kv_heads, (int64_t)a.pages_per_seq * a.page_size);
+  a.nsplits = p.nsplits;
+  a.row_tiles = p.row_tiles;
   void* kargs[] = {&a};
   const int64_t grid = (int64_t)a.batch * a.kv_heads * a.row_tiles * a.nsplits;
-  const hipError_t e = hipLaunchKernel(rows_kernel(a.head_dim), dim3((unsigned)grid), dim3(64 * kRowsWaves), kargs, 0, stream);
+  const hipError_t e =
+      hipLaunchKernel(p.few ? tokens_kernel(a.head_dim) : rows_kernel(a.head_dim), dim3((unsigned)grid),
+                      dim3(64 * (p.few ? kTokenWaves : kRowsWaves)), kargs, 0, stream);
   if (e != hipSuccess || a.nsplits == 1) return e;
   const int64_t per = (int64_t)a.max_q * a.q_heads * (a.head_dim >> 3);
   return hipLaunchKernel((const void*)&attn_join_kernel, dim3((unsigned)((per + 255) / 256), (unsigned)a.batch),

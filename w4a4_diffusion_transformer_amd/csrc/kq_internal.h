@@ -182,10 +182,16 @@ struct AttnArgs {
   float c;  // scale * log2(e)
 };
 
-// Key ranges the launch divides each sequence into (1: no workspace), and the workspace bytes that takes.
-int attn_splits(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t capacity);
+// How a call is divided: the kernel for few rows or the one for many, tiles of rows, and ranges of keys (more than
+// one: partial results in a workspace, joined by a second launch).
+struct AttnPlan {
+  bool few;
+  int row_tiles, nsplits;
+};
+
+AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t capacity);
 int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, int nsplits);
-hipError_t launch_attn(const AttnArgs& args, int nsplits, hipStream_t stream);
+hipError_t launch_attn(const AttnArgs& args, hipStream_t stream);
 
 hipError_t launch_cache(bool write, bool both, const CacheArgs& args, hipStream_t stream);
 hipError_t launch_gemm(const GemmArgs& args, hipStream_t stream);
