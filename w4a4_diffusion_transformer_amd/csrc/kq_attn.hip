@@ -38,6 +38,8 @@ namespace {
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 
+constexpr int kShareBatch = 1024;  // sequences up to which ranges are balanced over the batch
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -90,15 +92,22 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
   return s;
 }
 
-// Slot of key `key` of sequence b, or -1 where there is none: past the
-// length, or on a page that the cache does not have.
-__device__ __forceinline__ int slot_of(const AttnArgs& a, int b, int key, int len) {
-  if (key >= len) return -1;
+// The table entry of key `key` of sequence b, as loaded.  Apart from slot_of, so that it can be asked
+// for well ahead: without a branch and with nothing that looks at it, the load stays in flight.  Keys
+// past the end read the last entry; without a table the word read (the sequence's length) is not used.
+__device__ __forceinline__ int page_entry(const AttnArgs& a, int b, int key) {
+  const int p = min((int)fast_div((unsigned)key, a.by_page), a.pages_per_seq - 1);
+  const int32_t* at = a.table ? a.table + (int64_t)b * a.pages_per_seq + p : a.kv_len + b;
+  return *at;
+}
+
+// Slot of key `key`, whose table entry is `entry`, or -1 where there is none: past the end, or on a
+// page that the cache does not have.
+__device__ __forceinline__ int slot_of(const AttnArgs& a, int b, int key, int entry, int end) {
   const int p = (int)fast_div((unsigned)key, a.by_page);
-  const int64_t at = (int64_t)b * a.pages_per_seq + p;
-  const int64_t page = a.table ? (int64_t)a.table[at] : at;
-  if (page < 0 || page >= a.n_pages) return -1;
-  return (int)page * a.page_size + (key - p * a.page_size);
+  const int64_t page = a.table ? (int64_t)entry : (int64_t)b * a.pages_per_seq + p;
+  const bool there = key < end && page >= 0 && page < a.n_pages;
+  return there ? (int)page * a.page_size + (key - p * a.page_size) : -1;
 }
 
 // Scores of NK tiles of 32 keys -> probabilities in bf16 (the B operand of
@@ -298,8 +307,9 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
   float m = -__builtin_inff(), l = 0.0f;
 
   if (key0 < key1) {
-    int slot = slot_of(a, b, key0 + lane, key1);
+    int entry = page_entry(a, b, key0 + lane), slot = slot_of(a, b, key0 + lane, entry, key1);
     uint64_t seen = __builtin_amdgcn_ballot_w64(slot >= 0), seen_next = 0;
+    entry = page_entry(a, b, key0 + kKeys + lane);
     load(slot);
     stage(0);
     __syncthreads();
@@ -307,8 +317,9 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
     for (int key = key0; key < key1; key += kKeys, buf ^= 1) {
       const bool more = key + kKeys < key1;  // uniform
       if (more) {
-        slot = slot_of(a, b, key + kKeys + lane, key1);
+        slot = slot_of(a, b, key + kKeys + lane, entry, key1);
         seen_next = __builtin_amdgcn_ballot_w64(slot >= 0);
+        entry = page_entry(a, b, key + 2 * kKeys + lane);
         load(slot);
       }
       if (seen != 0 && key <= upto_max) {
@@ -341,35 +352,90 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
 
 // ---------------------------------------------------------------- few rows
 
-// A workgroup owns up to 16 rows; its four waves take 64-key tiles in turn,
-// each with its own loads, softmax and O, and join at the end.  What bounds
-// it is reading the cache: every code is read once, straight into registers
-// in the operand order of v_mfma_f32_16x16x32_bf16 (lane l: key l % 16 and
-// the l / 16-th quarter of the head's channels, which at head_dim 128 is one
-// MX block: one 16-byte load and one scale byte), the next tile's while this
-// one is multiplied.  Values pass through a wave-private LDS tile for their
-// transposition (32 keys at a time), so no wave waits for another.  Key order
-// within a 32-key step of the second product: index j of quarter g is key
-// 4 g + j (j < 4) or 16 + 4 g + j - 4, the order S^T has.
-// The key heads of one sequence and range follow one another on one XCD: they
-// read neighbouring parts of the same cache lines.
+// A workgroup owns up to 16 rows of one or two key heads; its four waves take
+// tiles of keys in turn (64 of one head, 32 of two), each with its own loads,
+// softmax and O, and join at the end.  What bounds it is reading the cache:
+//  - Every code is read once into registers, the next tile's while this one
+//    is multiplied, and nothing looks at a loaded word before its use: a
+//    select or a branch on it would wait there.  Table entries are asked for
+//    two tiles ahead.
+//  - Adjacent lanes read a key's part of the row (at head_dim 128 a lane reads
+//    one MX block: 16 bytes and a scale byte), since loads are merged among
+//    adjacent lanes only: in the operand order of v_mfma_f32_16x16x32_bf16
+//    (lane l: key l % 16, the l / 16-th quarter of the channels) every lane
+//    was an access of its own, 64 an instruction, and the address units, busy
+//    80% of the time, were the bound (32 sequences of 8192 keys, 8 heads of
+//    128: 97 us; 87 so).
+//  - With two heads those reads are whole 128-byte lines: a compute unit has
+//    about as many requests in flight either way, so twice the bytes (75 us,
+//    3.9 TB/s; 256 sequences of 2048: 128 us, 4.5 TB/s, of the 5.1 to 5.9 that
+//    a plain read of as much reaches).
+// Keys change lanes as codes through LDS, values as bf16 for their
+// transposition (32 keys at a time), both in wave-private memory, so no wave
+// waits for another.  Key order within a 32-key step of the second product:
+// index j of quarter g is key 4 g + j (j < 4) or 16 + 4 g + j - 4, the order
+// S^T has.
 constexpr int kTokenRows = 16, kTokenWaves = 4;
+constexpr int64_t kTwoHeadKeys = int64_t(1) << 20;  // keys times heads from which a workgroup takes two heads
 
-template <int DP, bool ALIGNED>
-__global__ __launch_bounds__(64 * kTokenWaves, DP <= 64 ? 4 : 3) void attn_tokens_kernel(AttnArgs a) {
-  constexpr int NS = DP / 32, NO = DP / 16, VS = DP + 16, OS = DP + 4;
-  constexpr int kVBytes = kTokenWaves * 32 * VS * 2, kOBytes = kTokenWaves * kTokenRows * OS * 4;
+// Keys of one workgroup of a sequence that sees `see`: the smallest share
+// (in tiles of 64) by which the batch's keys are at most a.chunks pieces, the
+// workgroups of a group of heads that the GPU holds at once; so a ragged batch
+// is divided into equal pieces, in one round, whatever room its cache has.
+// More where the sequence has fewer ranges than that takes.  The same for
+// every workgroup of the sequence.
+__device__ __forceinline__ int token_share(const AttnArgs& a, int see, int unit, int lane) {
+  int share = (see + a.nsplits - 1) / a.nsplits;
+  if (a.nsplits > 1 && a.batch <= kShareBatch) {
+    auto total = [&](auto&& of) {  // sum over the batch; at most 2^21 tiles a sequence, 2^31 in all
+      unsigned n = 0;
+      for (int i = lane; i < a.batch; i += 64)
+        n += of(min((unsigned)(max(0, min(a.kv_len[i], a.capacity)) + 63) >> 6, 1u << 21));
+#pragma unroll
+      for (int x = 32; x; x >>= 1) n += __shfl_xor(n, x);
+      return n;
+    };
+    const unsigned tiles = total([](unsigned t) { return t; }), most = (unsigned)a.chunks;
+    const unsigned spare = (unsigned)max(a.chunks - a.batch, (a.chunks + 1) / 2);
+    unsigned lo = max(1u, (tiles + most - 1) / most), hi = max(lo, (tiles + spare - 1) / spare);
+#pragma unroll 1
+    for (int it = 0; it < 8 && lo < hi; ++it) {
+      const unsigned mid = (lo + hi) >> 1;
+      const float inv = 1.0f / (float)mid;  // pieces need not be counted exactly
+      if (total([&](unsigned t) { return (unsigned)ceilf((float)t * inv); }) <= most)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    share = max(share, (int)min(hi, 1u << 24) * 64);
+  }
+  share = __builtin_amdgcn_readfirstlane(share);
+  return (int)min(((int64_t)share + unit - 1) / unit * unit, (int64_t)1 << 30);
+}
+
+template <int DP, bool ALIGNED, int HEADS>
+__global__ __launch_bounds__(64 * kTokenWaves, 2) void attn_tokens_kernel(AttnArgs a) {
+  constexpr int NS = DP / 32, NO = DP / 16, NB = ALIGNED ? 1 : NS;
+  constexpr int KEYS = 64 / HEADS, KT = KEYS / 16;  // keys of a wave's tile, and in operand tiles of 16
+  constexpr int LANES = 4 * HEADS, STEP = 64 / LANES;  // lanes that read one key, keys that one load reads
+  constexpr int VS = HEADS * DP + 16, OS = DP + 4;     // LDS row strides: values (elements), outputs (floats)
+  constexpr int kVBytes = kTokenWaves * 32 * VS * 2, kOBytes = kTokenWaves * HEADS * kTokenRows * OS * 4;
   __shared__ __attribute__((aligned(16))) uint8_t shared[kVBytes > kOBytes ? kVBytes : kOBytes];
-  __shared__ float wave_m[kTokenWaves][kTokenRows], wave_l[kTokenWaves][kTokenRows];
+  __shared__ float wave_m[kTokenWaves][HEADS][kTokenRows], wave_l[kTokenWaves][HEADS][kTokenRows];
 
   const int tid = threadIdx.x, lane = tid & 63, quarter = lane >> 4, col = lane & 15;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int kvh = id % a.kv_heads;
-  id /= a.kv_heads;
-  const int tile = id % a.row_tiles;
-  id /= a.row_tiles;
-  const int split = id % a.nsplits, b = id / a.nsplits;
+  // Workgroups are dealt to the eight XCDs in turn: the head groups of one sequence and range follow one
+  // another on one XCD, sequences and ranges go round them (each range of a sequence on another); later
+  // ranges, which a short sequence does not have, come last, so that the workgroups that do work are
+  // spread evenly.
+  const int head_groups = a.kv_heads / HEADS, turn = blockIdx.x >> 3;
+  int id = turn / head_groups * 8 + (blockIdx.x & 7);
+  const int units = a.batch * a.row_tiles, split = id / units;
+  if (split >= a.nsplits) return;
+  const int kvh0 = turn % head_groups * HEADS;
+  id = (id % units + 3 * split) % units;
+  const int tile = id % a.row_tiles, b = id / a.row_tiles;
   const Seq sq = sequence(a, b);
   const int rows = min(sq.nq, a.max_q) * a.group;
   const int r0 = tile * kTokenRows;
@@ -377,188 +443,258 @@ __global__ __launch_bounds__(64 * kTokenWaves, DP <= 64 ? 4 : 3) void attn_token
 
   const int last_q = (int)fast_div((unsigned)(min(r0 + kTokenRows, rows) - 1), a.by_group);
   const int see = a.causal ? max(0, min(sq.len, sq.len - sq.nq + last_q + 1)) : sq.len;
-  const int share = ((see + a.nsplits - 1) / a.nsplits + 63) & ~63;
-  const int key0 = min(see, split * share), key1 = min(see, key0 + share);
+  const int share = token_share(a, see, KEYS * kTokenWaves, lane);
+  const int key0 = (int)min((int64_t)see, (int64_t)split * share), key1 = min(see, key0 + share);
 
   const int r = min(r0 + col, rows - 1);
   const int qi = (int)fast_div((unsigned)r, a.by_group);
-  const int head = kvh * a.group + (r - qi * a.group);
+  const int head = kvh0 * a.group + (r - qi * a.group);
   const int upto = a.causal ? sq.len - sq.nq + qi : sq.len;  // last key this lane's query sees
   const int upto_min = __builtin_amdgcn_readfirstlane(upto);
 
-  const int nc = a.head_dim >> 3, chunk0 = kvh * nc;
+  const int nc = a.head_dim >> 3, chunk0 = kvh0 * nc;
   const int64_t width8 = (int64_t)a.kv_heads * nc;
-  bf16x8 qf[NS];
-  const uint16_t* qp = a.q + (sq.row0 + qi) * a.q_stride + (int64_t)head * a.head_dim;
+  bf16x8 qf[HEADS][NS];
 #pragma unroll
-  for (int s = 0; s < NS; ++s) {
-    const int ch = quarter * NS + s;
-    u32x4 w = {0, 0, 0, 0};
-    if (ch < nc) w = *reinterpret_cast<const u32x4*>(qp + 8 * ch);
-    qf[s] = __builtin_bit_cast(bf16x8, w);
+  for (int h = 0; h < HEADS; ++h) {
+    const uint16_t* qp = a.q + (sq.row0 + qi) * a.q_stride + (int64_t)(head + h * a.group) * a.head_dim;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int ch = quarter * NS + s;
+      u32x4 w = {0, 0, 0, 0};
+      if (ch < nc) w = *reinterpret_cast<const u32x4*>(qp + 8 * ch);
+      qf[h][s] = __builtin_bit_cast(bf16x8, w);
+    }
   }
 
-  // One 64-key tile of this lane: codes and scales of keys 16 k + col.
+  // One tile as it is loaded: codes and scales of keys STEP k + lane / LANES, head and quarter
+  // lane % LANES.  Nothing may look at them before their use (a select here would wait for the loads): a
+  // key that is not there reads slot 0 (always there) and is dealt with in multiply(); a quarter's chunks
+  // past the head's read its first one (their queries are zero, and their channels of O are not stored).
   struct Tile {
     unsigned kw[4][NS], vw[4][NS];
-    unsigned kb[4][ALIGNED ? 1 : NS], vb[4][ALIGNED ? 1 : NS];
-    uint64_t seen;
+    unsigned kb[4][NB], vb[4][NB];
+    unsigned long long seen;
   };
+  const int lkey = lane / LANES, lc = lane % LANES, lq = lc & 3;
+  const int chunk = chunk0 + (lc >> 2) * nc;  // of the lane's head
   auto load = [&](int slot, Tile& t) {
     t.seen = __builtin_amdgcn_ballot_w64(slot >= 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int sl = __shfl(slot, 16 * k + col);
-      const int64_t at = (int64_t)max(sl, 0) * width8 + chunk0 + quarter * NS;  // slot 0 is always there
+      const int64_t at = (int64_t)max(__shfl(slot, STEP * k + lkey), 0) * width8 + chunk;
       if constexpr (ALIGNED) {
         typedef __attribute__((ext_vector_type(NS))) unsigned words;
-        const words kw = *reinterpret_cast<const words*>(a.k_codes + 4 * at);
-        const words vw = *reinterpret_cast<const words*>(a.v_codes + 4 * at);
-        t.kb[k][0] = a.k_scales[at >> 2];
-        t.vb[k][0] = sl >= 0 ? a.v_scales[at >> 2] : 0u;
+        const int64_t c = at + lq * NS;
+        const words kw = *reinterpret_cast<const words*>(a.k_codes + 4 * c);
+        const words vw = *reinterpret_cast<const words*>(a.v_codes + 4 * c);
+        t.kb[k][0] = a.k_scales[c >> 2];
+        t.vb[k][0] = a.v_scales[c >> 2];
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           t.kw[k][s] = kw[s];
-          t.vw[k][s] = sl >= 0 ? vw[s] : 0u;
+          t.vw[k][s] = vw[s];
         }
       } else {
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          const bool in = quarter * NS + s < nc;
-          const int64_t c = in ? at + s : 0;
-          t.kw[k][s] = in ? *reinterpret_cast<const unsigned*>(a.k_codes + 4 * c) : 0u;
-          t.kb[k][s] = in ? a.k_scales[c >> 2] : 0u;
-          t.vw[k][s] = in && sl >= 0 ? *reinterpret_cast<const unsigned*>(a.v_codes + 4 * c) : 0u;
-          t.vb[k][s] = in && sl >= 0 ? a.v_scales[c >> 2] : 0u;
+          const int64_t c = at + (lq * NS + s < nc ? lq * NS + s : 0);
+          t.kw[k][s] = *reinterpret_cast<const unsigned*>(a.k_codes + 4 * c);
+          t.kb[k][s] = a.k_scales[c >> 2];
+          t.vw[k][s] = *reinterpret_cast<const unsigned*>(a.v_codes + 4 * c);
+          t.vb[k][s] = a.v_scales[c >> 2];
         }
       }
     }
   };
 
-  f32x4 o[NO];
+  f32x4 o[HEADS][NO];
+  float m[HEADS], l[HEADS];
 #pragma unroll
-  for (int t = 0; t < NO; ++t) o[t] = f32x4{0, 0, 0, 0};
-  float m = -__builtin_inff(), l = 0.0f;
+  for (int h = 0; h < HEADS; ++h) {
+    m[h] = -__builtin_inff();
+    l[h] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NO; ++t) o[h][t] = f32x4{0, 0, 0, 0};
+  }
   uint16_t* vs = reinterpret_cast<uint16_t*>(shared) + wv * 32 * VS;
 
-  auto multiply = [&](const Tile& t, int key) {
-    f32x4 s[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s[k] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int d = 0; d < NS; ++d)
-        s[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_values8(t.kw[k][d], t.kb[k][ALIGNED ? 0 : d]), qf[d], s[k], 0,
-                                                       0, 0);
-    }
-    if (t.seen != ~(uint64_t)0 || upto_min < key + 63) {
-      const uint64_t mine = t.seen >> (4 * quarter);
+  auto multiply = [&](Tile& t, int key) {
+    constexpr unsigned long long kAll = HEADS == 1 ? ~0ull : (1ull << (KEYS & 63)) - 1;
+    const unsigned long long seen = t.seen & kAll;
+    if (seen != kAll) {  // values that are not there: zeros, whatever the slot holds
 #pragma unroll
       for (int k = 0; k < 4; ++k)
+        if (!((seen >> (STEP * k + lkey)) & 1)) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (!((mine >> (16 * k + x)) & 1) || key + 16 * k + 4 * quarter + x > upto) s[k][x] = -__builtin_inff();
+          for (int s = 0; s < NS; ++s) t.vw[k][s] = 0;
+#pragma unroll
+          for (int s = 0; s < NB; ++s) t.vb[k][s] = 0;
+        }
     }
-    float top = s[0][0];
+    // keys from the lanes that loaded them to the operand's: codes through LDS (pieces swizzled against
+    // bank conflicts), scale bytes, four to a register, by one permute
+    unsigned scales[HEADS][NB];
+    unsigned* kx = reinterpret_cast<unsigned*>(vs);
+    auto swizzle = [](int k) { return HEADS == 1 ? (k >> 1) & 3 : k & (LANES - 1); };
+#pragma unroll
+    for (int x = 0; x < NB; ++x) {
+      const unsigned w = t.kb[0][x] | (t.kb[1][x] << 8) | (t.kb[2][x] << 16) | (t.kb[3][x] << 24);
+#pragma unroll
+      for (int h = 0; h < HEADS; ++h)
+        scales[h][x] = (unsigned)__shfl((int)w, col % STEP * LANES + 4 * h + quarter);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) top = fmaxf(top, s[k][x]);
-    if (__builtin_amdgcn_ballot_w64(top > m) != 0) {  // some query has a new maximum
-      const unsigned u = __float_as_uint(top);
-      const auto h = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-      const float mn = fmaxf(m, swap_max32(fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]))));
-      const float alpha = mn > m ? __builtin_amdgcn_exp2f((m - mn) * a.c) : 1.0f;
-      l *= alpha;
+      for (int d = 0; d < NS; ++d)
+        kx[((STEP * k + lkey) * LANES + (lc ^ swizzle(STEP * k + lkey))) * NS + d] = t.kw[k][d];
+    wave_lds_fence();
+    f32x4 s[HEADS][KT];
 #pragma unroll
-      for (int d = 0; d < NO; ++d) o[d] *= alpha;
-      m = mn;
-    }
-    const float base = m == -__builtin_inff() ? 0.0f : m * a.c;
-    bf16x8 p[2];
-    float sum = 0.0f;
+    for (int h = 0; h < HEADS; ++h)
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][x], a.c, -base));
-        sum += e;
-        p[k >> 1][4 * (k & 1) + x] = (__bf16)e;
-      }
-    l += sum;
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < KT; ++k) {
+        // key 16 k + col was byte (16 k + col) / STEP of its lane
+        const unsigned shift = 8 * ((16 / STEP) * k + col / STEP);
+        s[h][k] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int d = 0; d < NS; ++d)
-          *reinterpret_cast<bf16x8*>(&vs[(16 * k + col) * VS + 8 * (quarter * NS + d)]) =
-              mx_values8(t.vw[2 * half + k][d], t.vb[2 * half + k][ALIGNED ? 0 : d]);
-      wave_lds_fence();
-      const uint16_t* at = vs + (4 * quarter + (col >> 2)) * VS + 4 * (col & 3);
+          s[h][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              mx_values8(kx[((16 * k + col) * LANES + ((4 * h + quarter) ^ swizzle(16 * k + col))) * NS + d],
+                         (scales[h][ALIGNED ? 0 : d] >> shift) & 0xFF),
+              qf[h][d], s[h][k], 0, 0, 0);
+      }
+    wave_lds_fence();
+    if (seen != kAll || upto_min < key + KEYS - 1) {
+      const unsigned long long mine = seen >> (4 * quarter);
 #pragma unroll
-      for (int d = 0; d < NO; ++d) {
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 16 * d));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 16 * VS + 16 * d));
-        const bf16x8 w = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, p[half], o[d], 0, 0, 0);
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (!((mine >> (16 * k + x)) & 1) || key + 16 * k + 4 * quarter + x > upto) {
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) s[h][k][x] = -__builtin_inff();
+          }
+    }
+    bf16x8 p[HEADS][KT / 2];
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) {
+      float top = s[h][0][0];
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top = fmaxf(top, s[h][k][x]);
+      if (__builtin_amdgcn_ballot_w64(top > m[h]) != 0) {  // some query has a new maximum
+        const unsigned u = __float_as_uint(top);
+        const auto y = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        const float mn = fmaxf(m[h], swap_max32(fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]))));
+        const float alpha = mn > m[h] ? __builtin_amdgcn_exp2f((m[h] - mn) * a.c) : 1.0f;
+        l[h] *= alpha;
+#pragma unroll
+        for (int d = 0; d < NO; ++d) o[h][d] *= alpha;
+        m[h] = mn;
+      }
+      const float base = m[h] == -__builtin_inff() ? 0.0f : m[h] * a.c;
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][k][x], a.c, -base));
+          sum += e;
+          p[h][k >> 1][4 * (k & 1) + x] = (__bf16)e;
+        }
+      l[h] += sum;
+    }
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+#pragma unroll
+    for (int part = 0; part < KT / 2; ++part) {  // 32 keys
+#pragma unroll
+      for (int k = 0; k < 32 / STEP; ++k)
+#pragma unroll
+        for (int d = 0; d < NS; ++d)
+          *reinterpret_cast<bf16x8*>(&vs[(STEP * k + lkey) * VS + (lc >> 2) * DP + 8 * (lq * NS + d)]) =
+              mx_values8(t.vw[32 / STEP * part + k][d], t.vb[32 / STEP * part + k][ALIGNED ? 0 : d]);
+      wave_lds_fence();
+#pragma unroll
+      for (int h = 0; h < HEADS; ++h) {
+        const uint16_t* at = vs + (4 * quarter + (col >> 2)) * VS + h * DP + 4 * (col & 3);
+#pragma unroll
+        for (int d = 0; d < NO; ++d) {
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 16 * d));
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 16 * VS + 16 * d));
+          const bf16x8 w = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          o[h][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, p[h][part], o[h][d], 0, 0, 0);
+        }
       }
       wave_lds_fence();
     }
   };
 
   // tiles wv, wv + 4, ... of the range: the next tile's codes are in flight during this one's
-  // product, and the slots of the one after
-  constexpr int kStep = 64 * kTokenWaves;
-  int key = key0 + 64 * wv;
+  // product, and the slots of the one after, asked for before those codes (loads return in order:
+  // behind them, waiting for a slot would wait for the codes too)
+  constexpr int kStep = KEYS * kTokenWaves;
+  int key = key0 + KEYS * wv;
   if (key < key1) {
-    Tile cur, next;
-    load(slot_of(a, b, key + lane, key1), cur);
-    int slot = slot_of(a, b, key + kStep + lane, key1);
-    for (; key + kStep < key1; key += kStep) {
-      load(slot, next);
-      slot = slot_of(a, b, key + 2 * kStep + lane, key1);
-      multiply(cur, key);
-      cur = next;
+    Tile even, odd;
+    auto entry = [&](int k) { return page_entry(a, b, k + lane % KEYS); };
+    auto slot = [&](int k, int e) { return slot_of(a, b, k + lane % KEYS, e, key1); };
+    int e0 = entry(key), e1 = entry(key + kStep);
+    load(slot(key, e0), even);
+    for (;; key += 2 * kStep) {
+      e0 = entry(key + 2 * kStep);
+      load(slot(key + kStep, e1), odd);
+      multiply(even, key);
+      if (key + kStep >= key1) break;
+      e1 = entry(key + 3 * kStep);
+      load(slot(key + 2 * kStep, e0), even);
+      multiply(odd, key + kStep);
+      if (key + 2 * kStep >= key1) break;
     }
-    multiply(cur, key);
   }
 
   // join the waves
-  l = quarter_sum(l);
-  if (quarter == 0) {
-    wave_m[wv][col] = m;
-    wave_l[wv][col] = l;
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    const float sum = quarter_sum(l[h]);
+    if (quarter == 0) {
+      wave_m[wv][h][col] = m[h];
+      wave_l[wv][h][col] = sum;
+    }
   }
   __syncthreads();  // also: every wave is done with its tile of values
-  float top = wave_m[0][col];
-#pragma unroll
-  for (int w = 1; w < kTokenWaves; ++w) top = fmaxf(top, wave_m[w][col]);
-  const float mine = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m - top) * a.c);
   float* os = reinterpret_cast<float*>(shared);
 #pragma unroll
-  for (int d = 0; d < NO; ++d)
-    *reinterpret_cast<f32x4*>(&os[(wv * kTokenRows + col) * OS + 16 * d + 4 * quarter]) = o[d] * mine;
-  __syncthreads();
-  for (int x = tid; x < kTokenRows * nc; x += 64 * kTokenWaves) {
-    const int q = x / nc, ch = x - q * nc;
-    if (r0 + q >= rows) break;
-    float best = wave_m[0][q];
+  for (int h = 0; h < HEADS; ++h) {
+    float top = wave_m[0][h][col];
 #pragma unroll
-    for (int w = 1; w < kTokenWaves; ++w) best = fmaxf(best, wave_m[w][q]);
+    for (int w = 1; w < kTokenWaves; ++w) top = fmaxf(top, wave_m[w][h][col]);
+    const float mine = m[h] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m[h] - top) * a.c);
+#pragma unroll
+    for (int d = 0; d < NO; ++d)
+      *reinterpret_cast<f32x4*>(&os[((wv * HEADS + h) * kTokenRows + col) * OS + 16 * d + 4 * quarter]) = o[h][d] * mine;
+  }
+  __syncthreads();
+  for (int x = tid; x < HEADS * kTokenRows * nc; x += 64 * kTokenWaves) {
+    const int hq = x / nc, ch = x - hq * nc, hw = hq / kTokenRows, q = hq % kTokenRows;
+    if (r0 + q >= rows) continue;
+    float best = wave_m[0][hw][q];
+#pragma unroll
+    for (int w = 1; w < kTokenWaves; ++w) best = fmaxf(best, wave_m[w][hw][q]);
     float sum = 0.0f;
     f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kTokenWaves; ++w) {
-      sum += wave_m[w][q] == -__builtin_inff() ? 0.0f
-                                               : wave_l[w][q] * __builtin_amdgcn_exp2f((wave_m[w][q] - best) * a.c);
-      const f32x4* src = reinterpret_cast<const f32x4*>(&os[(w * kTokenRows + q) * OS + 8 * ch]);
+      const float wm = wave_m[w][hw][q];
+      sum += wm == -__builtin_inff() ? 0.0f : wave_l[w][hw][q] * __builtin_amdgcn_exp2f((wm - best) * a.c);
+      const f32x4* src = reinterpret_cast<const f32x4*>(&os[((w * HEADS + hw) * kTokenRows + q) * OS + 8 * ch]);
       lo += src[0];
       hi += src[1];
     }
     const int qx = (int)fast_div((unsigned)(r0 + q), a.by_group);
-    const int h = kvh * a.group + (r0 + q - qx * a.group);
+    const int h = (kvh0 + hw) * a.group + (r0 + q - qx * a.group);
     const int64_t row = sq.row0 + qx;
     const float base = best == -__builtin_inff() ? best : best * a.c;
     if (a.nsplits > 1) {
@@ -568,6 +704,7 @@ __global__ __launch_bounds__(64 * kTokenWaves, DP <= 64 ? 4 : 3) void attn_token
         ml[0] = base;
         ml[1] = sum;
       }
+      if (sum == 0.0f) continue;  // the join reads no output of an empty range
       f32x4* dst = reinterpret_cast<f32x4*>(a.part + at * a.head_dim + 8 * ch);
       dst[0] = lo;
       dst[1] = hi;
@@ -588,43 +725,68 @@ __global__ __launch_bounds__(64 * kTokenWaves, DP <= 64 ? 4 : 3) void attn_token
 
 // ---------------------------------------------------------------- joining
 
-// One lane per eight channels of a row: the splits' outputs weighted by
-// exp2(max_s - max).
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int nc = a.head_dim >> 3;
-  const int64_t per = (int64_t)a.max_q * a.q_heads * nc;  // lanes of a sequence
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// The ranges' outputs weighted by exp2(max_s - max).  Sixteen lanes hold a
+// row's channels, eight each; `slices` such groups share a row's ranges (one
+// lane group reading 64 of them in turn took longer than the attention), and
+// meet in LDS in slice order.
+constexpr int kJoinThreads = 256;
+
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int slices) {
+  __shared__ float part[kJoinThreads][11];  // maximum, sum, eight channels, and a pad against bank conflicts
+  const int tid = threadIdx.x, lane = tid & 15, group = tid >> 4, slice = group % slices;
+  const int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 16 / slices) + group / slices;  // row and head of the sequence
   const int b = blockIdx.y;
-  if (i >= per) return;
   const Seq sq = sequence(a, b);
-  const int ch = (int)(i % nc);
-  const int64_t rh = i / nc;
-  const int head = (int)(rh % a.q_heads), qi = (int)(rh / a.q_heads);
-  if (qi >= sq.nq) return;
+  const int qi = (int)(i / a.q_heads), head = (int)(i - (int64_t)qi * a.q_heads);
+  const bool live = i < (int64_t)a.max_q * a.q_heads && qi < sq.nq && 8 * lane < a.head_dim;
   const int64_t n = a.q_rows * a.q_heads, at = (sq.row0 + qi) * a.q_heads + head;
   const float* ml = a.part + (int64_t)a.nsplits * n * a.head_dim;
-  float top = -__builtin_inff();
-  for (int s = 0; s < a.nsplits; ++s) top = fmaxf(top, ml[2 * (s * n + at)]);
-  float sum = 0.0f, o[8] = {};
-  for (int s = 0; s < a.nsplits; ++s) {
-    const float l = ml[2 * (s * n + at) + 1];
-    if (l == 0.0f) continue;
-    const float w = __builtin_amdgcn_exp2f(ml[2 * (s * n + at)] - top);
-    sum += w * l;
-    const f32x4* src = reinterpret_cast<const f32x4*>(a.part + (s * n + at) * a.head_dim + 8 * ch);
-    const f32x4 x = src[0], y = src[1];
+  float top = -__builtin_inff(), sum = 0.0f, o[8] = {};
+  if (live)
+#pragma unroll 4
+    for (int s = slice; s < a.nsplits; s += slices) {
+      const float ms = ml[2 * (s * n + at)], ls = ml[2 * (s * n + at) + 1];
+      if (ls == 0.0f) continue;  // an empty range: its output was not written
+      const f32x4* src = reinterpret_cast<const f32x4*>(a.part + (s * n + at) * a.head_dim + 8 * lane);
+      const f32x4 x = src[0], y = src[1];
+      const float t = fmaxf(top, ms);
+      const float keep = __builtin_amdgcn_exp2f(top - t), w = __builtin_amdgcn_exp2f(ms - t);
+      top = t;
+      sum = sum * keep + w * ls;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[k] += w * x[k];
-      o[4 + k] += w * y[k];
+      for (int k = 0; k < 4; ++k) {
+        o[k] = o[k] * keep + w * x[k];
+        o[4 + k] = o[4 + k] * keep + w * y[k];
+      }
+    }
+  if (slices > 1) {
+    part[tid][0] = top;
+    part[tid][1] = sum;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[tid][2 + k] = o[k];
+    __syncthreads();
+    if (slice != 0) return;
+    for (int s = 1; s < slices; ++s) top = fmaxf(top, part[tid + 16 * s][0]);
+    const float own = sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(part[tid][0] - top);
+    sum *= own;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] *= own;
+    for (int s = 1; s < slices; ++s) {
+      const float* p = part[tid + 16 * s];
+      if (p[1] == 0.0f) continue;
+      const float w = __builtin_amdgcn_exp2f(p[0] - top);
+      sum += w * p[1];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] += w * p[2 + k];
     }
   }
+  if (!live) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (a.lse && ch == 0) a.lse[at] = kLn2 * (top + __builtin_amdgcn_logf(sum));
+  if (a.lse && lane == 0) a.lse[at] = kLn2 * (top + __builtin_amdgcn_logf(sum));
   bf16x8 w;
 #pragma unroll
   for (int k = 0; k < 8; ++k) w[k] = (__bf16)(o[k] * inv);
-  *reinterpret_cast<u32x4*>(a.out + (sq.row0 + qi) * a.out_stride + (int64_t)head * a.head_dim + 8 * ch) =
+  *reinterpret_cast<u32x4*>(a.out + (sq.row0 + qi) * a.out_stride + (int64_t)head * a.head_dim + 8 * lane) =
       __builtin_bit_cast(u32x4, w);
 }
 
@@ -635,28 +797,48 @@ const void* rows_kernel(int d) {
                    : (const void*)&attn_rows_kernel<128>;
 }
 
+template <int HEADS>
 const void* tokens_kernel(int d) {
-  if (d == 32) return (const void*)&attn_tokens_kernel<32, true>;
-  if (d == 64) return (const void*)&attn_tokens_kernel<64, true>;
-  if (d == 128) return (const void*)&attn_tokens_kernel<128, true>;
-  return d < 32   ? (const void*)&attn_tokens_kernel<32, false>
-         : d < 64 ? (const void*)&attn_tokens_kernel<64, false>
-         : d <= 96 ? (const void*)&attn_tokens_kernel<96, false>
-                   : (const void*)&attn_tokens_kernel<128, false>;
+  if (d == 32) return (const void*)&attn_tokens_kernel<32, true, HEADS>;
+  if (d == 64) return (const void*)&attn_tokens_kernel<64, true, HEADS>;
+  if (d == 128) return (const void*)&attn_tokens_kernel<128, true, HEADS>;
+  return d < 32   ? (const void*)&attn_tokens_kernel<32, false, HEADS>
+         : d < 64 ? (const void*)&attn_tokens_kernel<64, false, HEADS>
+         : d <= 96 ? (const void*)&attn_tokens_kernel<96, false, HEADS>
+                   : (const void*)&attn_tokens_kernel<128, false, HEADS>;
 }
 
 }  // namespace
 
-// Few rows: up to two 16-row tiles for each sequence and key head.
-AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t capacity) {
-  AttnPlan p;
+// Few rows: up to two 16-row tiles for each sequence and key head.  Their
+// workgroups take four key heads where that leaves enough of them (the four
+// read the same cache lines together), else one, so that a short context is
+// spread over waves.
+AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                   int64_t capacity) {
+  AttnPlan p{};
   const int64_t rows = max_q * (q_heads / kv_heads);
   p.few = rows <= 2 * kTokenRows;
   const int tile = p.few ? kTokenRows : kRowsTile;
   p.row_tiles = (int)((rows + tile - 1) / tile);
-  const int64_t tiles = std::max<int64_t>(1, batch * kv_heads * p.row_tiles);
-  const int64_t want = (p.few ? 2048 : 512) / tiles, most = capacity / (p.few ? 256 : 128);
-  p.nsplits = (int)std::max<int64_t>(1, std::min(want, most));
+  p.wg_heads = 1;
+  if (p.few) {
+    const int64_t tiles = std::max<int64_t>(1, batch * kv_heads * p.row_tiles);
+    p.wg_heads = kv_heads % 2 == 0 && tiles * capacity >= kTwoHeadKeys ? 2 : 1;
+    const int64_t wgs = tiles / p.wg_heads, unit = 64 / p.wg_heads * kTokenWaves;
+    // Ranges of a sequence: up to one workgroup a compute unit as long as a wave has a tile, up to the two
+    // that fit while it has four; none below four tiles (the join costs as much: 512 keys of one sequence
+    // 7.9 us whole, 10.0 in two ranges; 4096 keys of eight sequences 20 us in four, 24 in eight).  Twice
+    // as many may be launched, for the longest sequences of a ragged batch.
+    const int64_t steps = capacity / unit;
+    const int64_t each = steps < 4 ? 1 : std::max(std::min(256 / wgs, steps), std::min(512 / wgs, steps / 4));
+    p.nsplits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * each, steps, 64}));
+    if (steps < 4) p.nsplits = 1;
+    p.chunks = (int)(std::max<int64_t>(1, each) * batch);
+  } else {
+    const int64_t tiles = std::max<int64_t>(1, batch * kv_heads * p.row_tiles);
+    p.nsplits = (int)std::max<int64_t>(1, std::min(512 / tiles, capacity / 128));
+  }
   return p;
 }
 
@@ -672,18 +854,25 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   a.capacity = a.n_pages > 0 ? a.pages_per_seq * a.page_size : 0;
   a.c = a.scale * kLog2e;
   const AttnPlan p =
-      attn_plan(a.batch, a.max_q, a.q_heads, a.kv_heads, (int64_t)a.pages_per_seq * a.page_size);
+      attn_plan(a.batch, a.max_q, a.q_heads, a.kv_heads, a.head_dim, (int64_t)a.pages_per_seq * a.page_size);
   a.nsplits = p.nsplits;
+  a.chunks = p.chunks;
   a.row_tiles = p.row_tiles;
   void* kargs[] = {&a};
-  const int64_t grid = (int64_t)a.batch * a.kv_heads * a.row_tiles * a.nsplits;
+  const int64_t units = (int64_t)a.batch * a.row_tiles * a.nsplits;
+  const int64_t grid = p.few ? (units + 7) / 8 * 8 * (a.kv_heads / p.wg_heads) : units * a.kv_heads;
   const hipError_t e =
-      hipLaunchKernel(p.few ? tokens_kernel(a.head_dim) : rows_kernel(a.head_dim), dim3((unsigned)grid),
-                      dim3(64 * (p.few ? kTokenWaves : kRowsWaves)), kargs, 0, stream);
+      hipLaunchKernel(!p.few            ? rows_kernel(a.head_dim)
+                      : p.wg_heads == 2 ? tokens_kernel<2>(a.head_dim)
+                                        : tokens_kernel<1>(a.head_dim),
+                      dim3((unsigned)grid), dim3(64 * (p.few ? kTokenWaves : kRowsWaves)), kargs, 0, stream);
   if (e != hipSuccess || a.nsplits == 1) return e;
-  const int64_t per = (int64_t)a.max_q * a.q_heads * (a.head_dim >> 3);
-  return hipLaunchKernel((const void*)&attn_join_kernel, dim3((unsigned)((per + 255) / 256), (unsigned)a.batch),
-                         dim3(256), kargs, 0, stream);
+  int slices = 1;
+  while (slices < 16 && slices < a.nsplits) slices *= 2;
+  const int64_t pairs = (int64_t)a.max_q * a.q_heads, per = kJoinThreads / 16 / slices;
+  void* jargs[] = {&a, &slices};
+  return hipLaunchKernel((const void*)&attn_join_kernel, dim3((unsigned)((pairs + per - 1) / per), (unsigned)a.batch),
+                         dim3(kJoinThreads), jargs, 0, stream);
 }
 
 }  // namespace kq
