@@ -90,6 +90,13 @@ def test_lengths(kv, q_len, causal):
     Case([q_len], [kv], 2, 1, 64, 48, seed=kv).check(causal=causal)
 
 
+@pytest.mark.parametrize("causal", [False, True])
+def test_more_tiles_than_the_gpu_holds(causal):
+    """Row tiles that run whole and, of the last, partial round, some whose keys are divided; sequences by length."""
+    Case([40] * 13, [130, 300, 0, 64, 257, 300, 1, 129, 290, 31, 200, 299, 128], 20, 20, 8, 16, seed=41).check(causal=causal)
+    Case([300, 7, 120], [70, 333, 128], 100, 100, 8, 16, seed=42).check(causal=causal)
+
+
 @pytest.mark.parametrize("page", [1, 3, 16, 50, 64, 300])
 def test_pages_that_end_inside_a_tile(page):
     Case([5, 130], [333, 290], 4, 2, 64, page, seed=page).check(causal=True)

@@ -606,7 +606,8 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
 int64_t kq_attention_mx_workspace(int64_t q_rows, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
                                   int64_t head_dim, int64_t capacity) {
   if (check_attention(q_rows, batch, max_q, q_heads, kv_heads, head_dim, capacity) != KQ_OK) return 0;
-  return kq::attn_workspace(q_rows, q_heads, head_dim, kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity).nsplits);
+  return kq::attn_workspace(q_rows, q_heads, head_dim,
+                            kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity));
 }
 
 kq_status kq_attention_mx(const uint16_t* Q, int64_t Q_stride, int64_t q_rows, const int32_t* q_start, int64_t batch,
@@ -632,8 +633,8 @@ kq_status kq_attention_mx(const uint16_t* Q, int64_t Q_stride, int64_t q_rows, c
       !aligned(V_scales, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(page_table, 4) ||
       !aligned(lse, 4) || !aligned(workspace, 16))
     return KQ_ERR_ALIGN;
-  const int nsplits = kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity).nsplits;
-  const int64_t need = kq::attn_workspace(q_rows, q_heads, head_dim, nsplits);
+  const int64_t need = kq::attn_workspace(q_rows, q_heads, head_dim,
+                                          kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity));
   if (need > 0 && (!workspace || workspace_bytes < need)) return KQ_ERR_WORKSPACE;
   const uint64_t nc = (uint64_t)n_slots * (uint64_t)(kv_heads * head_dim) / 2;
   const Range outs[] = {{out, strided_bytes(q_rows, out_stride, q_width)},

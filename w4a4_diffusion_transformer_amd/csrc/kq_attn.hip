@@ -176,17 +176,206 @@ __device__ __forceinline__ void add_pv(f32x16 (&o)[NT], const uint16_t* v, int s
   }
 }
 
-// Writes a lane's query: the output and lse, or, in a split launch, this
-// range's unnormalised output, maximum (in log2 units) and sum.
-template <int NT>
-__device__ __forceinline__ void store_row(const AttnArgs& a, const f32x16 (&o)[NT], float m, float l, int64_t row,
-                                          int head, int split, int half, bool live) {
-  if (!live) return;
+// What a workgroup of the many-rows kernel does.  Tiles are ranked by what
+// they are likely to cost, for the longest to start first: by the sequence's
+// keys (of up to 64 sequences), then by their place in it, last first (with a
+// causal mask the last see the most keys).  The first a.whole ranks are
+// workgroups of their own, each of the rest (the last, partial round of the
+// GPU) is divided into a.nsplits key ranges, whose results are joined.
+struct RowsWork {
+  int b, kvh, tile;
+  int index, split, splits;  // of a divided tile: its number among those, its range, and of how many
+};
+
+__device__ __forceinline__ RowsWork rows_work(const AttnArgs& a, int id) {
+  RowsWork w;
+  w.index = 0;
+  w.split = 0;
+  w.splits = 1;
+  int rank = id;
+  if (id >= a.whole) {
+    w.index = (id - a.whole) % a.split_tiles;
+    w.split = (id - a.whole) / a.split_tiles;
+    w.splits = a.nsplits;
+    rank = a.whole + w.index;
+  }
+  const int each = a.row_tiles * a.kv_heads, order = rank / each, rest = rank - order * each;
+  w.tile = a.row_tiles - 1 - rest / a.kv_heads;
+  w.kvh = rest % a.kv_heads;
+  w.b = order;
+  if (a.batch > 1 && a.batch <= 64) {  // the order-th sequence by length
+    const int i = threadIdx.x & 63, len = i < a.batch ? a.kv_len[i] : 0;
+    int longer = 0;
+    for (int j = 0; j < a.batch; ++j) {
+      const int other = __builtin_amdgcn_readlane(len, j);
+      longer += other > len || (other == len && j < i);
+    }
+    w.b = __builtin_ctzll(__builtin_amdgcn_ballot_w64(i < a.batch && longer == order));
+  }
+  return w;
+}
+
+// ---------------------------------------------------------------- many rows
+
+// A workgroup owns 256 rows, 32 to each of its eight waves, over the same
+// keys.  Tiles of 64 keys are widened once per workgroup into LDS, row-major
+// and padded so that fragment reads and transposing reads fall on distinct
+// banks; waves 0-3 widen keys, waves 4-7 values, a thread the quarter of one
+// key's channels.  Two LDS buffers: the codes of tile t + 1 are loaded before
+// tile t is multiplied and widened after it, the table entries of tile t + 2
+// asked for before those loads.
+constexpr int kRowsWaves = 8, kRowsTile = 32 * kRowsWaves, kKeys = 64;
+
+template <int DP, bool ALIGNED>
+__global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs a) {
+  constexpr int KS = DP + 8, VS = DP + 16, OS = DP + 8;  // row strides of keys, values, outputs in LDS, elements
+  constexpr int NT = DP / 32, ND = DP / 16, NS = DP / 32, NB = ALIGNED ? 1 : NS;
+  constexpr int kTile = kKeys * (KS + VS);  // elements of a buffer: keys, then values
+  static_assert(kRowsTile * OS <= 2 * kTile, "the outputs fit the tiles");
+  __shared__ __attribute__((aligned(16))) uint16_t tiles[2 * kTile];
+
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const RowsWork w = rows_work(a, blockIdx.x);
+  const Seq sq = sequence(a, w.b);
+  const int rows = min(sq.nq, a.max_q) * a.group;
+  const int r0 = w.tile * kRowsTile;
+  if (r0 >= rows) return;
+
+  // keys of this workgroup: what its last query sees, this range's share of it
+  const int last_q = (int)fast_div((unsigned)(min(r0 + kRowsTile, rows) - 1), a.by_group);
+  const int see = a.causal ? max(0, min(sq.len, sq.len - sq.nq + last_q + 1)) : sq.len;
+  const int share = ((see + w.splits - 1) / w.splits + kKeys - 1) & ~(kKeys - 1);
+  const int key0 = min(see, w.split * share), key1 = min(see, key0 + share);
+
+  const int r = r0 + 32 * wv + col;
+  const bool live = r < rows;
+  const int qi = (int)fast_div((unsigned)min(r, rows - 1), a.by_group);
+  const int head = w.kvh * a.group + (min(r, rows - 1) - qi * a.group);
+  const int64_t row = sq.row0 + qi;
+  const int upto = a.causal ? sq.len - sq.nq + qi : sq.len;  // last key this query sees
+  const int upto_min = __builtin_amdgcn_readfirstlane(upto);  // rows ascend, lane 0 has the first query
+  const int upto_max = __builtin_amdgcn_readlane(upto, 31);
+
+  bf16x8 qf[ND];
+  const uint16_t* qp = a.q + row * a.q_stride + (int64_t)head * a.head_dim;
+#pragma unroll
+  for (int s = 0; s < ND; ++s) {
+    const int d = 16 * s + 8 * half;
+    u32x4 x = {0, 0, 0, 0};
+    if (live && d < a.head_dim) x = *reinterpret_cast<const u32x4*>(qp + d);
+    qf[s] = __builtin_bit_cast(bf16x8, x);
+  }
+
+  // This thread's part of a tile: key tid / 4 % 64, quarter tid % 4 of its channels.  As loaded; a key
+  // that is not there reads slot 0 (always there), a quarter's chunks past the head's its first one.
+  const int nc = a.head_dim >> 3, chunk0 = w.kvh * nc;
+  const int64_t width8 = (int64_t)a.kv_heads * nc;
+  const bool values = wv >= kRowsWaves / 2;  // uniform
+  const uint8_t* codes = values ? a.v_codes : a.k_codes;
+  const uint8_t* scales = values ? a.v_scales : a.k_scales;
+  const int lkey = (tid >> 2) & (kKeys - 1), lq = tid & 3;
+  unsigned word[NS], byte[NB];
+  auto load = [&](int slot) {
+    const int64_t at = (int64_t)max(__shfl(slot, lkey), 0) * width8 + chunk0;
+    if constexpr (ALIGNED) {
+      typedef __attribute__((ext_vector_type(NS))) unsigned words;
+      const int64_t c = at + lq * NS;
+      const words x = *reinterpret_cast<const words*>(codes + 4 * c);
+      byte[0] = scales[c >> 2];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) word[s] = x[s];
+    } else {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int64_t c = at + (lq * NS + s < nc ? lq * NS + s : 0);
+        word[s] = *reinterpret_cast<const unsigned*>(codes + 4 * c);
+        byte[s] = scales[c >> 2];
+      }
+    }
+  };
+  uint16_t* mine = tiles + (values ? kKeys * KS + lkey * VS : lkey * KS) + 8 * NS * lq;
+  auto stage = [&](int buf, uint64_t seen) {
+    if (seen != ~(uint64_t)0 && !((seen >> lkey) & 1)) {  // a key that is not there: zeros, whatever the slot holds
+#pragma unroll
+      for (int s = 0; s < NS; ++s) word[s] = 0;
+#pragma unroll
+      for (int s = 0; s < NB; ++s) byte[s] = 0;
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      // chunks past the head's are zeros in the keys (their queries are too, but 0 * inf is not)
+      const bool pad = !ALIGNED && lq * NS + s >= nc;
+      *reinterpret_cast<bf16x8*>(mine + buf * kTile + 8 * s) =
+          mx_values8(pad ? 0u : word[s], pad ? 0u : byte[ALIGNED ? 0 : s]);
+    }
+  };
+
+  f32x16 o[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int x = 0; x < 16; ++x) o[t][x] = 0.0f;
+  float m = -__builtin_inff(), l = 0.0f;
+
+  if (key0 < key1) {
+    int slot = slot_of(a, w.b, key0 + lane, page_entry(a, w.b, key0 + lane), key1);
+    int entry = page_entry(a, w.b, key0 + kKeys + lane);
+    uint64_t seen = __builtin_amdgcn_ballot_w64(slot >= 0), seen_next = 0;
+    load(slot);
+    stage(0, seen);
+    __syncthreads();
+    int buf = 0;
+    for (int key = key0; key < key1; key += kKeys, buf ^= 1) {
+      const bool more = key + kKeys < key1;  // uniform
+      if (more) {
+        slot = slot_of(a, w.b, key + kKeys + lane, entry, key1);
+        seen_next = __builtin_amdgcn_ballot_w64(slot >= 0);
+        entry = page_entry(a, w.b, key + 2 * kKeys + lane);
+        load(slot);
+      }
+      if (seen != 0 && key <= upto_max) {
+        const uint16_t* ks = tiles + buf * kTile;
+        const uint16_t* vs = ks + kKeys * KS;
+        f32x16 s[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) s[k][x] = 0.0f;
+        // the wave in its products goes before the one in its softmax on the same SIMD: 1-3%
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&ks[(32 * k + col) * KS + 16 * d + 8 * half]);
+            s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[d], s[k], 0, 0, 0);
+          }
+        if (seen != ~(uint64_t)0 || upto_min < key + kKeys - 1) mask_scores<2>(s, seen, upto - key, half);
+        bf16x8 p[4];
+        __builtin_amdgcn_s_setprio(0);
+        softmax_step<2, NT>(s, a.c, m, l, o, p);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) add_pv<NT>(o, vs + 16 * x * VS, VS, p[x], lane);
+        __builtin_amdgcn_s_setprio(0);
+      }
+      if (more) {
+        stage(buf ^ 1, seen_next);
+        __syncthreads();
+        seen = seen_next;
+      }
+    }
+  }
+  l = swap_sum32(l);
   const float base = m == -__builtin_inff() ? m : m * a.c;
-  if (a.nsplits > 1) {
-    const int64_t n = a.q_rows * a.q_heads, at = split * n + row * a.q_heads + head;
+
+  if (w.splits > 1) {  // this range's unnormalised output, maximum (in log2 units) and sum
+    const int64_t n = (int64_t)a.split_tiles * w.splits * kRowsTile;
+    const int64_t at = ((int64_t)w.index * w.splits + w.split) * kRowsTile + 32 * wv + col;
+    if (!live) return;
     if (half == 0) {
-      float* ml = a.part + (int64_t)a.nsplits * n * a.head_dim + 2 * at;
+      float* ml = a.part + n * a.head_dim + 2 * at;
       ml[0] = base;
       ml[1] = l;
     }
@@ -202,152 +391,32 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const f32x16 (&o)[N
       }
     return;
   }
+
+  if (a.lse && half == 0 && live) a.lse[row * a.q_heads + head] = kLn2 * (base + __builtin_amdgcn_logf(l));
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // an empty row: zeros
-  if (a.lse && half == 0) a.lse[row * a.q_heads + head] = kLn2 * (base + __builtin_amdgcn_logf(l));
-  uint16_t* dst = a.out + row * a.out_stride + (int64_t)head * a.head_dim;
+  // through LDS, so that a wave stores whole rows
+  __syncthreads();  // every wave is done with the tiles
+  uint16_t* os = tiles + 32 * wv * OS;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int d = 32 * t + 8 * g + 4 * half;
-      if (d < a.head_dim) {
-        typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
-        const bf16x4 w = {(__bf16)(o[t][4 * g] * inv), (__bf16)(o[t][4 * g + 1] * inv),
-                          (__bf16)(o[t][4 * g + 2] * inv), (__bf16)(o[t][4 * g + 3] * inv)};
-        *reinterpret_cast<u32x2*>(dst + d) = __builtin_bit_cast(u32x2, w);
-      }
+      typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+      const bf16x4 x = {(__bf16)(o[t][4 * g] * inv), (__bf16)(o[t][4 * g + 1] * inv), (__bf16)(o[t][4 * g + 2] * inv),
+                        (__bf16)(o[t][4 * g + 3] * inv)};
+      *reinterpret_cast<u32x2*>(&os[col * OS + 32 * t + 8 * g + 4 * half]) = __builtin_bit_cast(u32x2, x);
     }
-}
-
-// ---------------------------------------------------------------- many rows
-
-// Workgroup: 4 waves of 32 rows over the same keys.  Tiles of 64 keys are
-// widened once per workgroup into LDS (row-major, padded so that fragment
-// reads and transposing reads fall on distinct banks), double buffered: the
-// codes of tile t + 1 are loaded before tile t is multiplied and widened after.
-constexpr int kRowsWaves = 4, kRowsTile = 32 * kRowsWaves, kKeys = 64;
-
-template <int DP>
-__global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs a) {
-  constexpr int KS = DP + 8, VS = DP + 16;  // row strides of the staged tiles, elements
-  constexpr int NT = DP / 32, ND = DP / 16, NC = DP / 8, U = kKeys * NC / (64 * kRowsWaves);
-  __shared__ __attribute__((aligned(16))) uint16_t ks[2][kKeys * KS];
-  __shared__ __attribute__((aligned(16))) uint16_t vs[2][kKeys * VS];
-
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int split = id % a.nsplits;
-  id /= a.nsplits;
-  const int tile = id % a.row_tiles;
-  id /= a.row_tiles;
-  const int kvh = id % a.kv_heads, b = id / a.kv_heads;
-  const Seq sq = sequence(a, b);
-  const int rows = min(sq.nq, a.max_q) * a.group;
-  const int r0 = tile * kRowsTile;
-  if (r0 >= rows) return;
-
-  // keys of this workgroup: what its last query sees, this split's share of it
-  const int last_q = (int)fast_div((unsigned)(min(r0 + kRowsTile, rows) - 1), a.by_group);
-  const int see = a.causal ? max(0, min(sq.len, sq.len - sq.nq + last_q + 1)) : sq.len;
-  const int share = ((see + a.nsplits - 1) / a.nsplits + kKeys - 1) & ~(kKeys - 1);
-  const int key0 = split * share, key1 = min(see, key0 + share);
-
-  const int r = r0 + 32 * wv + col;
-  const bool live = r < rows;
-  const int qi = (int)fast_div((unsigned)min(r, rows - 1), a.by_group);
-  const int head = kvh * a.group + (min(r, rows - 1) - qi * a.group);
-  const int64_t row = sq.row0 + qi;
-  const int upto = a.causal ? sq.len - sq.nq + qi : sq.len;  // last key this query sees
-  const int upto_min = __builtin_amdgcn_readfirstlane(upto);  // rows ascend, lane 0 has the first query
-  const int upto_max = __builtin_amdgcn_readlane(upto, 31);
-
-  bf16x8 qf[ND];
-  const uint16_t* qp = a.q + row * a.q_stride + (int64_t)head * a.head_dim;
+  wave_lds_fence();
+  constexpr int LPR = DP / 8, RPI = 64 / LPR;  // lanes of a row, rows of an instruction
+  const int ch = lane % LPR;
 #pragma unroll
-  for (int s = 0; s < ND; ++s) {
-    const int d = 16 * s + 8 * half;
-    u32x4 w = {0, 0, 0, 0};
-    if (live && d < a.head_dim) w = *reinterpret_cast<const u32x4*>(qp + d);
-    qf[s] = __builtin_bit_cast(bf16x8, w);
+  for (int k = 0; k < (32 + RPI - 1) / RPI; ++k) {
+    const int x = k * RPI + lane / LPR, y = r0 + 32 * wv + x;  // row of the wave, packed row
+    if (lane >= LPR * RPI || x >= 32 || y >= rows || ch >= nc) continue;
+    const int q = (int)fast_div((unsigned)y, a.by_group), h = w.kvh * a.group + (y - q * a.group);
+    *reinterpret_cast<u32x4*>(a.out + (sq.row0 + q) * a.out_stride + (int64_t)h * a.head_dim + 8 * ch) =
+        *reinterpret_cast<const u32x4*>(&os[x * OS + 8 * ch]);
   }
-
-  const int chunk0 = kvh * (a.head_dim >> 3);      // the head's first 8-channel chunk in a slot's row
-  const int nc = a.head_dim >> 3;
-  const int64_t width8 = (int64_t)a.kv_heads * nc;  // chunks of a slot's row
-  unsigned kw[U], kb[U], vw[U], vb[U];
-  // Lane l looks up key l of the tile; the unit (key, chunk) u * 256 + tid takes its slot from there.
-  auto load = [&](int slot) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int unit = u * (64 * kRowsWaves) + tid, key = unit / NC, ch = unit % NC;
-      const int sl = __shfl(slot, key);
-      const bool in = sl >= 0 && ch < nc;
-      const int64_t at = in ? (int64_t)sl * width8 + chunk0 + ch : 0;  // slot 0 is always there
-      kw[u] = in ? *reinterpret_cast<const unsigned*>(a.k_codes + 4 * at) : 0u;
-      kb[u] = in ? a.k_scales[at >> 2] : 0u;
-      vw[u] = in ? *reinterpret_cast<const unsigned*>(a.v_codes + 4 * at) : 0u;
-      vb[u] = in ? a.v_scales[at >> 2] : 0u;
-    }
-  };
-  auto stage = [&](int buf) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int unit = u * (64 * kRowsWaves) + tid, key = unit / NC, ch = unit % NC;
-      *reinterpret_cast<bf16x8*>(&ks[buf][key * KS + 8 * ch]) = mx_values8(kw[u], kb[u]);
-      *reinterpret_cast<bf16x8*>(&vs[buf][key * VS + 8 * ch]) = mx_values8(vw[u], vb[u]);
-    }
-  };
-
-  f32x16 o[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int x = 0; x < 16; ++x) o[t][x] = 0.0f;
-  float m = -__builtin_inff(), l = 0.0f;
-
-  if (key0 < key1) {
-    int entry = page_entry(a, b, key0 + lane), slot = slot_of(a, b, key0 + lane, entry, key1);
-    uint64_t seen = __builtin_amdgcn_ballot_w64(slot >= 0), seen_next = 0;
-    entry = page_entry(a, b, key0 + kKeys + lane);
-    load(slot);
-    stage(0);
-    __syncthreads();
-    int buf = 0;
-    for (int key = key0; key < key1; key += kKeys, buf ^= 1) {
-      const bool more = key + kKeys < key1;  // uniform
-      if (more) {
-        slot = slot_of(a, b, key + kKeys + lane, entry, key1);
-        seen_next = __builtin_amdgcn_ballot_w64(slot >= 0);
-        entry = page_entry(a, b, key + 2 * kKeys + lane);
-        load(slot);
-      }
-      if (seen != 0 && key <= upto_max) {
-        f32x16 s[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) s[k][x] = 0.0f;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&ks[buf][(32 * k + col) * KS + 16 * d + 8 * half]);
-            s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[d], s[k], 0, 0, 0);
-          }
-        }
-        if (seen != ~(uint64_t)0 || upto_min < key + kKeys - 1) mask_scores<2>(s, seen, upto - key, half);
-        bf16x8 p[4];
-        softmax_step<2, NT>(s, a.c, m, l, o, p);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) add_pv<NT>(o, &vs[buf][16 * x * VS], VS, p[x], lane);
-      }
-      if (more) {
-        stage(buf ^ 1);
-        __syncthreads();
-        seen = seen_next;
-      }
-    }
-  }
-  store_row<NT>(a, o, m, swap_sum32(l), row, head, split, half, live);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -731,23 +800,49 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void attn_tokens_kernel(AttnAr
 // meet in LDS in slice order.
 constexpr int kJoinThreads = 256;
 
+template <bool FEW>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int slices) {
   __shared__ float part[kJoinThreads][11];  // maximum, sum, eight channels, and a pad against bank conflicts
   const int tid = threadIdx.x, lane = tid & 15, group = tid >> 4, slice = group % slices;
-  const int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 16 / slices) + group / slices;  // row and head of the sequence
-  const int b = blockIdx.y;
+  const int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 16 / slices) + group / slices;
+  // the row's place in the output, and its partial results: the first one, and how far to the next
+  int b, qi, head;
+  bool live;
+  int64_t first, next, total;
+  if constexpr (FEW) {  // i: query and head of sequence blockIdx.y; results by range, row and head
+    b = blockIdx.y;
+    qi = (int)(i / a.q_heads);
+    head = (int)(i - (int64_t)qi * a.q_heads);
+    live = i < (int64_t)a.max_q * a.q_heads;
+  } else {  // i: row of the divided tiles; results by tile, range and row
+    const int index = (int)(i / kRowsTile), lr = (int)(i % kRowsTile);
+    const RowsWork w = rows_work(a, a.whole + min(index, a.split_tiles - 1));
+    const int r = w.tile * kRowsTile + lr;
+    b = w.b;
+    qi = (int)fast_div((unsigned)r, a.by_group);
+    head = w.kvh * a.group + (r - qi * a.group);
+    live = index < a.split_tiles && qi < a.max_q;
+    first = (int64_t)index * a.nsplits * kRowsTile + lr;
+    next = kRowsTile;
+    total = (int64_t)a.split_tiles * a.nsplits * kRowsTile;
+  }
   const Seq sq = sequence(a, b);
-  const int qi = (int)(i / a.q_heads), head = (int)(i - (int64_t)qi * a.q_heads);
-  const bool live = i < (int64_t)a.max_q * a.q_heads && qi < sq.nq && 8 * lane < a.head_dim;
-  const int64_t n = a.q_rows * a.q_heads, at = (sq.row0 + qi) * a.q_heads + head;
-  const float* ml = a.part + (int64_t)a.nsplits * n * a.head_dim;
+  live = live && qi < sq.nq && 8 * lane < a.head_dim;
+  const int64_t at = (sq.row0 + qi) * a.q_heads + head;
+  if constexpr (FEW) {
+    first = at;
+    next = a.q_rows * a.q_heads;
+    total = a.nsplits * next;
+  }
+  const float* ml = a.part + total * a.head_dim;
   float top = -__builtin_inff(), sum = 0.0f, o[8] = {};
   if (live)
 #pragma unroll 4
     for (int s = slice; s < a.nsplits; s += slices) {
-      const float ms = ml[2 * (s * n + at)], ls = ml[2 * (s * n + at) + 1];
+      const int64_t x0 = first + s * next;
+      const float ms = ml[2 * x0], ls = ml[2 * x0 + 1];
       if (ls == 0.0f) continue;  // an empty range: its output was not written
-      const f32x4* src = reinterpret_cast<const f32x4*>(a.part + (s * n + at) * a.head_dim + 8 * lane);
+      const f32x4* src = reinterpret_cast<const f32x4*>(a.part + x0 * a.head_dim + 8 * lane);
       const f32x4 x = src[0], y = src[1];
       const float t = fmaxf(top, ms);
       const float keep = __builtin_amdgcn_exp2f(top - t), w = __builtin_amdgcn_exp2f(ms - t);
@@ -791,10 +886,13 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
 }
 
 const void* rows_kernel(int d) {
-  return d <= 32   ? (const void*)&attn_rows_kernel<32>
-         : d <= 64 ? (const void*)&attn_rows_kernel<64>
-         : d <= 96 ? (const void*)&attn_rows_kernel<96>
-                   : (const void*)&attn_rows_kernel<128>;
+  if (d == 32) return (const void*)&attn_rows_kernel<32, true>;
+  if (d == 64) return (const void*)&attn_rows_kernel<64, true>;
+  if (d == 128) return (const void*)&attn_rows_kernel<128, true>;
+  return d < 32   ? (const void*)&attn_rows_kernel<32, false>
+         : d < 64 ? (const void*)&attn_rows_kernel<64, false>
+         : d <= 96 ? (const void*)&attn_rows_kernel<96, false>
+                   : (const void*)&attn_rows_kernel<128, false>;
 }
 
 template <int HEADS>
@@ -836,14 +934,18 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
     if (steps < 4) p.nsplits = 1;
     p.chunks = (int)(std::max<int64_t>(1, each) * batch);
   } else {
-    const int64_t tiles = std::max<int64_t>(1, batch * kv_heads * p.row_tiles);
-    p.nsplits = (int)std::max<int64_t>(1, std::min(512 / tiles, capacity / 128));
+    const int64_t tiles = batch * kv_heads * p.row_tiles, slots = 256;  // one workgroup a compute unit
+    const int64_t rest = tiles % slots;
+    p.nsplits = rest == 0 ? 1 : (int)std::max<int64_t>(1, std::min(slots / rest, capacity / (2 * kKeys)));
+    p.split_tiles = p.nsplits > 1 ? (int)rest : 0;
+    p.whole = (int)(tiles - p.split_tiles);
   }
   return p;
 }
 
-int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, int nsplits) {
-  return nsplits > 1 ? nsplits * q_rows * q_heads * (head_dim + 2) * 4 : 0;
+int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, const AttnPlan& p) {
+  if (p.nsplits <= 1) return 0;
+  return p.nsplits * (p.few ? q_rows * q_heads : (int64_t)p.split_tiles * kRowsTile) * (head_dim + 2) * 4;
 }
 
 hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
@@ -857,10 +959,12 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
       attn_plan(a.batch, a.max_q, a.q_heads, a.kv_heads, a.head_dim, (int64_t)a.pages_per_seq * a.page_size);
   a.nsplits = p.nsplits;
   a.chunks = p.chunks;
+  a.whole = p.whole;
+  a.split_tiles = p.split_tiles;
   a.row_tiles = p.row_tiles;
   void* kargs[] = {&a};
-  const int64_t units = (int64_t)a.batch * a.row_tiles * a.nsplits;
-  const int64_t grid = p.few ? (units + 7) / 8 * 8 * (a.kv_heads / p.wg_heads) : units * a.kv_heads;
+  int64_t grid = a.whole + (int64_t)a.split_tiles * a.nsplits;
+  if (p.few) grid = ((int64_t)a.batch * a.row_tiles * a.nsplits + 7) / 8 * 8 * (a.kv_heads / p.wg_heads);
   const hipError_t e =
       hipLaunchKernel(!p.few            ? rows_kernel(a.head_dim)
                       : p.wg_heads == 2 ? tokens_kernel<2>(a.head_dim)
@@ -869,10 +973,12 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   if (e != hipSuccess || a.nsplits == 1) return e;
   int slices = 1;
   while (slices < 16 && slices < a.nsplits) slices *= 2;
-  const int64_t pairs = (int64_t)a.max_q * a.q_heads, per = kJoinThreads / 16 / slices;
+  const int64_t per = kJoinThreads / 16 / slices;
+  const int64_t pairs = p.few ? (int64_t)a.max_q * a.q_heads : (int64_t)a.split_tiles * kRowsTile;
   void* jargs[] = {&a, &slices};
-  return hipLaunchKernel((const void*)&attn_join_kernel, dim3((unsigned)((pairs + per - 1) / per), (unsigned)a.batch),
-                         dim3(kJoinThreads), jargs, 0, stream);
+  return hipLaunchKernel(p.few ? (const void*)&attn_join_kernel<true> : (const void*)&attn_join_kernel<false>,
+                         dim3((unsigned)((pairs + per - 1) / per), p.few ? (unsigned)a.batch : 1u), dim3(kJoinThreads),
+                         jargs, 0, stream);
 }
 
 }  // namespace kq

@@ -178,7 +178,7 @@ struct AttnArgs {
   float* part;  // workspace of a split launch
   // set by the launch
   Divisor by_page, by_group;
-  int capacity, group, row_tiles, nsplits, chunks;
+  int capacity, group, row_tiles, nsplits, chunks, whole, split_tiles;
   float c;  // scale * log2(e)
 };
 
@@ -189,11 +189,12 @@ struct AttnPlan {
   int row_tiles, nsplits;
   int wg_heads;  // key heads of a workgroup
   int chunks;    // few: key ranges of the whole batch, for each group of heads
+  int whole, split_tiles;  // many: tiles that are not divided, and the others
 };
 
 AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                    int64_t capacity);
-int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, int nsplits);
+int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, const AttnPlan& plan);
 hipError_t launch_attn(const AttnArgs& args, hipStream_t stream);
 
 hipError_t launch_cache(bool write, bool both, const CacheArgs& args, hipStream_t stream);
