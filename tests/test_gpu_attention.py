@@ -95,6 +95,7 @@ def test_more_tiles_than_the_gpu_holds(causal):
     """Row tiles that run whole and, of the last, partial round, some whose keys are divided; sequences by length."""
     Case([40] * 13, [130, 300, 0, 64, 257, 300, 1, 129, 290, 31, 200, 299, 128], 20, 20, 8, 16, seed=41).check(causal=causal)
     Case([300, 7, 120], [70, 333, 128], 100, 100, 8, 16, seed=42).check(causal=causal)
+    Case([40] * 7, [600, 300, 0, 64, 257, 513, 129], 40, 40, 8, 16, seed=43).check(causal=causal)
 
 
 @pytest.mark.parametrize("page", [1, 3, 16, 50, 64, 300])
@@ -108,6 +109,20 @@ def test_pages_that_end_inside_a_tile(page):
 def test_ragged_batches_and_empty_sequences(q_len, causal):
     """Sequences without keys, without queries, and (causal) with fewer keys than queries; rows behind the last."""
     Case(q_len, [700, 64, 0, 31, 5], 8, 2, 128, 16, seed=3, tail=3).check(causal=causal)
+
+
+@pytest.mark.parametrize("dim,kv", [(32, 512), (64, 512), (64, 513), (72, 320), (72, 321), (112, 256), (128, 256), (128, 257)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_around_what_local_memory_holds(dim, kv, causal):
+    """Keys that just fit beside one another on chip, and one more; several groups of rows to a workgroup."""
+    kv_heads = 4 if dim in (72, 112) else 1
+    Case([600, 33], [kv, kv - 65], kv_heads, kv_heads, dim, 16, seed=dim, tail=1).check(causal=causal)
+
+
+def test_many_rows_over_few_keys():
+    """Enough rows that a workgroup takes several runs of them: 8 x 1111 rows of 24 heads over up to 70 keys."""
+    c = Case([1111] * 8, [70, 1, 0, 64, 65, 33, 17, 69], 24, 24, 64, 70, seed=51)
+    c.check()
 
 
 def test_uniform_batch_without_table_or_starts():

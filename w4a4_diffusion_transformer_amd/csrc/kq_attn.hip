@@ -145,24 +145,31 @@ __device__ __forceinline__ void softmax_step(f32x16 (&s)[NK], float c, float& m,
   l += sum;
 }
 
-// Masks scores: bit x of `seen` (wave-uniform) says whether the tile's key x
-// is there, `upto` is the last key of the tile that this lane's query sees.
+// Masks scores: `upto` is the last key of the tile that this lane's query sees; where the tile has keys
+// that are not there before that (holes: a page that the cache does not have), bit x of `seen`
+// (wave-uniform) says whether key x is.
 template <int NK>
-__device__ __forceinline__ void mask_scores(f32x16 (&s)[NK], uint64_t seen, int upto, int half) {
+__device__ __forceinline__ void mask_scores(f32x16 (&s)[NK], uint64_t seen, bool holes, int upto, int half) {
+  const int last = upto - 4 * half;
 #pragma unroll
   for (int k = 0; k < NK; ++k)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int x = 32 * k + 8 * (r >> 2) + (r & 3);  // key of half 0; half 1 has x + 4
-      const bool there = half ? (seen >> (x + 4)) & 1 : (seen >> x) & 1;
-      if (!there || x + 4 * half > upto) s[k][r] = -__builtin_inff();
-    }
+    for (int r = 0; r < 16; ++r)  // key of half 0; half 1 has 4 more
+      if (32 * k + 8 * (r >> 2) + (r & 3) > last) s[k][r] = -__builtin_inff();
+  if (holes) {
+    const uint64_t mine = seen >> (4 * half);
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (!((mine >> (32 * k + 8 * (r >> 2) + (r & 3))) & 1)) s[k][r] = -__builtin_inff();
+  }
 }
 
-// Adds P V of one 16-key step: V rows at `v` (this step's first key), row
+// V^T of one 16-key step as the A operands of O^T's NT tiles: V rows at `v` (the step's first key), row
 // stride `stride` elements.
 template <int NT>
-__device__ __forceinline__ void add_pv(f32x16 (&o)[NT], const uint16_t* v, int stride, const bf16x8& p, int lane) {
+__device__ __forceinline__ void read_values(const uint16_t* v, int stride, int lane, bf16x8 (&w)[NT]) {
   typedef __attribute__((address_space(3))) s16x4 lds4;
   const int g = lane >> 4, i = lane & 15;
   // 16 lanes: key rows 4 h .. 4 h + 3 (and + 8), columns 16 (g % 2) .. + 15 of each 32-column tile
@@ -171,8 +178,7 @@ __device__ __forceinline__ void add_pv(f32x16 (&o)[NT], const uint16_t* v, int s
   for (int t = 0; t < NT; ++t) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 32 * t));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + 8 * stride + 32 * t));
-    const bf16x8 w = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, p, o[t], 0, 0, 0);
+    w[t] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 }
 
@@ -217,22 +223,136 @@ __device__ __forceinline__ RowsWork rows_work(const AttnArgs& a, int id) {
 
 // ---------------------------------------------------------------- many rows
 
-// A workgroup owns 256 rows, 32 to each of its eight waves, over the same
-// keys.  Tiles of 64 keys are widened once per workgroup into LDS, row-major
-// and padded so that fragment reads and transposing reads fall on distinct
-// banks; waves 0-3 widen keys, waves 4-7 values, a thread the quarter of one
-// key's channels.  Two LDS buffers: the codes of tile t + 1 are loaded before
-// tile t is multiplied and widened after it, the table entries of tile t + 2
-// asked for before those loads.
+// A tile of 64 keys and values in LDS, row-major bf16, rows padded so that
+// fragment reads (keys) and transposing reads (values) fall on distinct banks,
+// and a thread's part in bringing it there: waves 0-3 widen keys, waves 4-7
+// values, a thread one quarter of key tid / 4 % 64's channels.
 constexpr int kRowsWaves = 8, kRowsTile = 32 * kRowsWaves, kKeys = 64;
 
 template <int DP, bool ALIGNED>
-__global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs a) {
-  constexpr int KS = DP + 8, VS = DP + 16, OS = DP + 8;  // row strides of keys, values, outputs in LDS, elements
-  constexpr int NT = DP / 32, ND = DP / 16, NS = DP / 32, NB = ALIGNED ? 1 : NS;
-  constexpr int kTile = kKeys * (KS + VS);  // elements of a buffer: keys, then values
-  static_assert(kRowsTile * OS <= 2 * kTile, "the outputs fit the tiles");
-  __shared__ __attribute__((aligned(16))) uint16_t tiles[2 * kTile];
+struct KeyTile {
+  static constexpr int KS = DP + 8, VS = DP + 16;      // row strides, elements
+  static constexpr int kSize = kKeys * (KS + VS);      // elements: keys, then values
+  static constexpr int NS = DP / 32, NB = ALIGNED ? 1 : NS;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t width8;
+  int chunk0, nc, lkey, lq, at;  // at: the thread's place in a tile
+  unsigned word[NS], byte[NB];   // as loaded
+
+  __device__ __forceinline__ void place(const AttnArgs& a, int kvh, int tid, int wv) {
+    const bool values = wv >= kRowsWaves / 2;  // uniform
+    codes = values ? a.v_codes : a.k_codes;
+    scales = values ? a.v_scales : a.k_scales;
+    nc = a.head_dim >> 3;
+    chunk0 = kvh * nc;
+    width8 = (int64_t)a.kv_heads * nc;
+    lkey = (tid >> 2) & (kKeys - 1);
+    lq = tid & 3;
+    at = (values ? kKeys * KS + lkey * VS : lkey * KS) + 8 * NS * lq;
+  }
+
+  // slot: of key `lane` of the tile.  A key that is not there reads slot 0 (always there), a quarter's
+  // chunks past the head's its first one; nothing looks at the words before stage().
+  __device__ __forceinline__ void load(int slot) {
+    const int64_t row = (int64_t)max(__shfl(slot, lkey), 0) * width8 + chunk0;
+    if constexpr (ALIGNED) {
+      typedef __attribute__((ext_vector_type(NS))) unsigned words;
+      const int64_t c = row + lq * NS;
+      const words x = *reinterpret_cast<const words*>(codes + 4 * c);
+      byte[0] = scales[c >> 2];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) word[s] = x[s];
+    } else {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int64_t c = row + (lq * NS + s < nc ? lq * NS + s : 0);
+        word[s] = *reinterpret_cast<const unsigned*>(codes + 4 * c);
+        byte[s] = scales[c >> 2];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void stage(uint16_t* tile, uint64_t seen) {
+    if (seen != ~(uint64_t)0 && !((seen >> lkey) & 1)) {  // a key that is not there: zeros, whatever the slot holds
+#pragma unroll
+      for (int s = 0; s < NS; ++s) word[s] = 0;
+#pragma unroll
+      for (int s = 0; s < NB; ++s) byte[s] = 0;
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const bool pad = !ALIGNED && lq * NS + s >= nc;  // chunks past the head's: zeros
+      *reinterpret_cast<bf16x8*>(tile + at + 8 * s) = mx_values8(pad ? 0u : word[s], pad ? 0u : byte[ALIGNED ? 0 : s]);
+    }
+  }
+};
+
+// One tile for the 32 rows of a wave: scores, softmax, and P V added to O^T.
+template <int DP>
+__device__ __forceinline__ void attend_tile(const uint16_t* ks, const bf16x8 (&qf)[DP / 16], uint64_t seen, int key,
+                                            int upto, int upto_min, int upto_max, float c, int lane, float& m,
+                                            float& l,
+                                            f32x16 (&o)[DP / 32]) {
+  constexpr int KS = KeyTile<DP, false>::KS, VS = KeyTile<DP, false>::VS;
+  const int half = lane >> 5, col = lane & 31;
+  const uint16_t* vs = ks + kKeys * KS;
+  f32x16 s[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int x = 0; x < 16; ++x) s[k][x] = 0.0f;
+  // the wave in its products goes before the one in its softmax on the same SIMD: 1-3%
+  __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+  for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&ks[(32 * k + col) * KS + 16 * d + 8 * half]);
+      s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[d], s[k], 0, 0, 0);
+    }
+  // a hole: some key under the highest that is there, or under the last that a query sees, is not
+  const bool holes = (seen & (seen + 1)) != 0 || (seen != ~(uint64_t)0 && upto_max >= key + __builtin_popcountll(seen));
+  if (holes || upto_min < key + kKeys - 1) mask_scores<2>(s, seen, holes, upto - key, half);
+  bf16x8 p[4], w[2][DP / 32];
+  __builtin_amdgcn_s_setprio(0);
+  read_values<DP / 32>(vs, VS, lane, w[0]);  // a step's values are read while the one before is multiplied
+  softmax_step<2, DP / 32>(s, c, m, l, o, p);
+  __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if (x < 3) read_values<DP / 32>(vs + 16 * (x + 1) * VS, VS, lane, w[(x + 1) & 1]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[x & 1][t], p[x], o[t], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __builtin_amdgcn_s_setprio(0);
+}
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  const uint64_t hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(v >> 32));
+  return (hi << 32) | (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)v);
+}
+
+// Four values of O^T from register r on, scaled, in bf16.
+__device__ __forceinline__ u32x2 pack4(const f32x16& o, int r, float inv) {
+  typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+  const bf16x4 x = {(__bf16)(o[r] * inv), (__bf16)(o[r + 1] * inv), (__bf16)(o[r + 2] * inv), (__bf16)(o[r + 3] * inv)};
+  return __builtin_bit_cast(u32x2, x);
+}
+
+// A workgroup owns 256 rows, 32 to each of its eight waves, over the same
+// keys; tiles are widened once for all of them.  Two LDS buffers: the codes of
+// tile t + 1 are loaded before tile t is multiplied and widened after it, the
+// table entries of tile t + 2 asked for before those loads.
+template <int DP, bool ALIGNED>
+__global__ __launch_bounds__(64 * kRowsWaves) __attribute__((amdgpu_waves_per_eu(DP <= 64 ? 4 : 2, DP <= 64 ? 4 : 2)))
+void attn_rows_kernel(AttnArgs a) {
+  using T = KeyTile<DP, ALIGNED>;
+  constexpr int NT = DP / 32, ND = DP / 16, OS = DP + 8;  // OS: row stride of the outputs in LDS, elements
+  static_assert(kRowsTile * OS <= 2 * T::kSize, "the outputs fit the tiles");
+  __shared__ __attribute__((aligned(16))) uint16_t tiles[2 * T::kSize];
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -253,7 +373,7 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
   const int qi = (int)fast_div((unsigned)min(r, rows - 1), a.by_group);
   const int head = w.kvh * a.group + (min(r, rows - 1) - qi * a.group);
   const int64_t row = sq.row0 + qi;
-  const int upto = a.causal ? sq.len - sq.nq + qi : sq.len;  // last key this query sees
+  const int upto = a.causal ? sq.len - sq.nq + qi : sq.len - 1;  // last key this query sees
   const int upto_min = __builtin_amdgcn_readfirstlane(upto);  // rows ascend, lane 0 has the first query
   const int upto_max = __builtin_amdgcn_readlane(upto, 31);
 
@@ -267,50 +387,8 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
     qf[s] = __builtin_bit_cast(bf16x8, x);
   }
 
-  // This thread's part of a tile: key tid / 4 % 64, quarter tid % 4 of its channels.  As loaded; a key
-  // that is not there reads slot 0 (always there), a quarter's chunks past the head's its first one.
-  const int nc = a.head_dim >> 3, chunk0 = w.kvh * nc;
-  const int64_t width8 = (int64_t)a.kv_heads * nc;
-  const bool values = wv >= kRowsWaves / 2;  // uniform
-  const uint8_t* codes = values ? a.v_codes : a.k_codes;
-  const uint8_t* scales = values ? a.v_scales : a.k_scales;
-  const int lkey = (tid >> 2) & (kKeys - 1), lq = tid & 3;
-  unsigned word[NS], byte[NB];
-  auto load = [&](int slot) {
-    const int64_t at = (int64_t)max(__shfl(slot, lkey), 0) * width8 + chunk0;
-    if constexpr (ALIGNED) {
-      typedef __attribute__((ext_vector_type(NS))) unsigned words;
-      const int64_t c = at + lq * NS;
-      const words x = *reinterpret_cast<const words*>(codes + 4 * c);
-      byte[0] = scales[c >> 2];
-#pragma unroll
-      for (int s = 0; s < NS; ++s) word[s] = x[s];
-    } else {
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int64_t c = at + (lq * NS + s < nc ? lq * NS + s : 0);
-        word[s] = *reinterpret_cast<const unsigned*>(codes + 4 * c);
-        byte[s] = scales[c >> 2];
-      }
-    }
-  };
-  uint16_t* mine = tiles + (values ? kKeys * KS + lkey * VS : lkey * KS) + 8 * NS * lq;
-  auto stage = [&](int buf, uint64_t seen) {
-    if (seen != ~(uint64_t)0 && !((seen >> lkey) & 1)) {  // a key that is not there: zeros, whatever the slot holds
-#pragma unroll
-      for (int s = 0; s < NS; ++s) word[s] = 0;
-#pragma unroll
-      for (int s = 0; s < NB; ++s) byte[s] = 0;
-    }
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      // chunks past the head's are zeros in the keys (their queries are too, but 0 * inf is not)
-      const bool pad = !ALIGNED && lq * NS + s >= nc;
-      *reinterpret_cast<bf16x8*>(mine + buf * kTile + 8 * s) =
-          mx_values8(pad ? 0u : word[s], pad ? 0u : byte[ALIGNED ? 0 : s]);
-    }
-  };
-
+  T part;
+  part.place(a, w.kvh, tid, wv);
   f32x16 o[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -322,8 +400,8 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
     int slot = slot_of(a, w.b, key0 + lane, page_entry(a, w.b, key0 + lane), key1);
     int entry = page_entry(a, w.b, key0 + kKeys + lane);
     uint64_t seen = __builtin_amdgcn_ballot_w64(slot >= 0), seen_next = 0;
-    load(slot);
-    stage(0, seen);
+    part.load(slot);
+    part.stage(tiles, seen);
     __syncthreads();
     int buf = 0;
     for (int key = key0; key < key1; key += kKeys, buf ^= 1) {
@@ -332,36 +410,12 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
         slot = slot_of(a, w.b, key + kKeys + lane, entry, key1);
         seen_next = __builtin_amdgcn_ballot_w64(slot >= 0);
         entry = page_entry(a, w.b, key + 2 * kKeys + lane);
-        load(slot);
+        part.load(slot);
       }
-      if (seen != 0 && key <= upto_max) {
-        const uint16_t* ks = tiles + buf * kTile;
-        const uint16_t* vs = ks + kKeys * KS;
-        f32x16 s[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) s[k][x] = 0.0f;
-        // the wave in its products goes before the one in its softmax on the same SIMD: 1-3%
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&ks[(32 * k + col) * KS + 16 * d + 8 * half]);
-            s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[d], s[k], 0, 0, 0);
-          }
-        if (seen != ~(uint64_t)0 || upto_min < key + kKeys - 1) mask_scores<2>(s, seen, upto - key, half);
-        bf16x8 p[4];
-        __builtin_amdgcn_s_setprio(0);
-        softmax_step<2, NT>(s, a.c, m, l, o, p);
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) add_pv<NT>(o, vs + 16 * x * VS, VS, p[x], lane);
-        __builtin_amdgcn_s_setprio(0);
-      }
+      if (seen != 0 && key <= upto_max)
+        attend_tile<DP>(tiles + buf * T::kSize, qf, seen, key, upto, upto_min, upto_max, a.c, lane, m, l, o);
       if (more) {
-        stage(buf ^ 1, seen_next);
+        part.stage(tiles + (buf ^ 1) * T::kSize, seen_next);
         __syncthreads();
         seen = seen_next;
       }
@@ -401,14 +455,11 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
-      const bf16x4 x = {(__bf16)(o[t][4 * g] * inv), (__bf16)(o[t][4 * g + 1] * inv), (__bf16)(o[t][4 * g + 2] * inv),
-                        (__bf16)(o[t][4 * g + 3] * inv)};
-      *reinterpret_cast<u32x2*>(&os[col * OS + 32 * t + 8 * g + 4 * half]) = __builtin_bit_cast(u32x2, x);
+      *reinterpret_cast<u32x2*>(&os[col * OS + 32 * t + 8 * g + 4 * half]) = pack4(o[t], 4 * g, inv);
     }
   wave_lds_fence();
   constexpr int LPR = DP / 8, RPI = 64 / LPR;  // lanes of a row, rows of an instruction
-  const int ch = lane % LPR;
+  const int ch = lane % LPR, nc = a.head_dim >> 3;
 #pragma unroll
   for (int k = 0; k < (32 + RPI - 1) / RPI; ++k) {
     const int x = k * RPI + lane / LPR, y = r0 + 32 * wv + x;  // row of the wave, packed row
@@ -416,6 +467,109 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void attn_rows_kernel(AttnArgs 
     const int q = (int)fast_div((unsigned)y, a.by_group), h = w.kvh * a.group + (y - q * a.group);
     *reinterpret_cast<u32x4*>(a.out + (sq.row0 + q) * a.out_stride + (int64_t)h * a.head_dim + 8 * ch) =
         *reinterpret_cast<const u32x4*>(&os[x * OS + 8 * ch]);
+  }
+}
+
+// ---------------------------------------------------------------- many rows, few keys
+
+// Cross attention to a short text: all keys and values of a sequence and head
+// fit in LDS, so a workgroup widens them once and its waves then work through
+// 32-row groups of their own with no barrier: wave w takes groups w, w + W, ...
+// of the workgroup's.  What bounds it is latency along a group's chain of
+// products and exponentials: as many waves as registers allow.  (Staged again
+// for every 256 rows, the 1152-wide transformer's 8 x 4096 rows over up to 300
+// keys took 106 us: most of it the start and end of workgroups.)
+constexpr int resident_tiles(int dp) { return dp <= 64 ? 8 : dp <= 96 ? 5 : 4; }      // of 64 keys, as LDS allows
+constexpr int resident_waves(int dp) { return dp <= 64 ? 16 : dp <= 96 ? 12 : 8; }  // as registers allow
+
+template <int DP, bool ALIGNED>
+__global__ __launch_bounds__(64 * resident_waves(DP))
+    __attribute__((amdgpu_waves_per_eu(resident_waves(DP) / 4, resident_waves(DP) / 4)))
+void attn_resident_kernel(AttnArgs a) {
+  using T = KeyTile<DP, ALIGNED>;
+  constexpr int NT = DP / 32, ND = DP / 16, NBUF = resident_tiles(DP);
+  __shared__ __attribute__((aligned(16))) uint16_t tiles[NBUF * T::kSize];
+  __shared__ uint64_t tile_seen[NBUF];
+
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const RowsWork w = rows_work(a, blockIdx.x);
+  const Seq sq = sequence(a, w.b);
+  const int rows = min(sq.nq, a.max_q) * a.group;
+  const int r0 = w.tile * 32 * a.run_groups;
+  if (r0 >= rows) return;
+  const int groups = min(a.run_groups, (rows - r0 + 31) >> 5);
+
+  // every tile's table entries, then codes, in flight at once
+  const int nt = (sq.len + kKeys - 1) / kKeys;  // at most NBUF: the capacity is
+  if (wv < kRowsWaves) {
+    int entry[NBUF];
+#pragma unroll
+    for (int t = 0; t < NBUF; ++t) entry[t] = page_entry(a, w.b, t * kKeys + lane);
+    T parts[NBUF];
+    uint64_t seen[NBUF];
+#pragma unroll
+    for (int t = 0; t < NBUF; ++t)
+      if (t < nt) {
+        const int slot = slot_of(a, w.b, t * kKeys + lane, entry[t], sq.len);
+        seen[t] = __builtin_amdgcn_ballot_w64(slot >= 0);
+        parts[t].place(a, w.kvh, tid, wv);
+        parts[t].load(slot);
+      }
+#pragma unroll
+    for (int t = 0; t < NBUF; ++t)
+      if (t < nt) {
+        if (tid == 0) tile_seen[t] = seen[t];
+        parts[t].stage(tiles + t * T::kSize, seen[t]);
+      }
+  }
+  __syncthreads();
+
+  for (int g = wv; g < groups; g += resident_waves(DP)) {
+    const int r = r0 + 32 * g + col;
+    const bool live = r < rows;
+    const int qi = (int)fast_div((unsigned)min(r, rows - 1), a.by_group);
+    const int head = w.kvh * a.group + (min(r, rows - 1) - qi * a.group);
+    const int64_t row = sq.row0 + qi;
+    const int upto = a.causal ? sq.len - sq.nq + qi : sq.len - 1;  // last key this query sees
+    const int upto_min = __builtin_amdgcn_readfirstlane(upto);
+    const int upto_max = __builtin_amdgcn_readlane(upto, 31);
+    bf16x8 qf[ND];
+    const uint16_t* qp = a.q + row * a.q_stride + (int64_t)head * a.head_dim;
+#pragma unroll
+    for (int s = 0; s < ND; ++s) {
+      const int d = 16 * s + 8 * half;
+      // chunks past the head's read its first one: their keys are zeros
+      qf[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(qp + (d < a.head_dim ? d : 0)));
+    }
+    f32x16 o[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[t][x] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;
+    for (int t = 0; t < nt; ++t) {
+      if (t * kKeys > upto_max) break;
+      attend_tile<DP>(tiles + t * T::kSize, qf, uniform64(tile_seen[t]), t * kKeys, upto, upto_min, upto_max, a.c,
+                      lane, m, l, o);
+    }
+    l = swap_sum32(l);
+    if (a.lse && half == 0 && live)
+      a.lse[row * a.q_heads + head] = kLn2 * ((m == -__builtin_inff() ? m : m * a.c) + __builtin_amdgcn_logf(l));
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // an empty row: zeros
+    // O^T holds a row's channels 8 g + 4 h + 0 .. 3 in half h: one exchange between the halves for each
+    // pair of g makes them 16 bytes, channels 16 p + 8 h + 0 .. 7
+    uint16_t* dst = a.out + row * a.out_stride + (int64_t)head * a.head_dim + 8 * half;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const u32x2 e = pack4(o[t], 8 * p, inv), f = pack4(o[t], 8 * p + 4, inv);
+        const auto x = __builtin_amdgcn_permlane32_swap(e[0], f[0], false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(e[1], f[1], false, false);
+        if (live && 32 * t + 16 * p + 8 * half < a.head_dim)
+          *reinterpret_cast<u32x4*>(dst + 32 * t + 16 * p) = u32x4{x[0], y[0], x[1], y[1]};
+      }
   }
 }
 
@@ -895,6 +1049,16 @@ const void* rows_kernel(int d) {
                    : (const void*)&attn_rows_kernel<128, false>;
 }
 
+const void* resident_kernel(int d) {
+  if (d == 32) return (const void*)&attn_resident_kernel<32, true>;
+  if (d == 64) return (const void*)&attn_resident_kernel<64, true>;
+  if (d == 128) return (const void*)&attn_resident_kernel<128, true>;
+  return d < 32   ? (const void*)&attn_resident_kernel<32, false>
+         : d < 64 ? (const void*)&attn_resident_kernel<64, false>
+         : d <= 96 ? (const void*)&attn_resident_kernel<96, false>
+                   : (const void*)&attn_resident_kernel<128, false>;
+}
+
 template <int HEADS>
 const void* tokens_kernel(int d) {
   if (d == 32) return (const void*)&attn_tokens_kernel<32, true, HEADS>;
@@ -907,6 +1071,8 @@ const void* tokens_kernel(int d) {
 }
 
 }  // namespace
+
+constexpr int64_t kResidentWgs = 384;
 
 // Few rows: up to two 16-row tiles for each sequence and key head.  Their
 // workgroups take four key heads where that leaves enough of them (the four
@@ -933,6 +1099,13 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
     p.nsplits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * each, steps, 64}));
     if (steps < 4) p.nsplits = 1;
     p.chunks = (int)(std::max<int64_t>(1, each) * batch);
+  } else if (capacity <= kKeys * resident_tiles((int)head_dim)) {
+    // runs of 256 rows, several where that leaves some three workgroups for each compute unit
+    const int64_t waves = resident_waves((int)head_dim), tiles = batch * kv_heads * ((rows + 32 * waves - 1) / (32 * waves));
+    p.run_groups = (int)(waves * std::max<int64_t>(1, std::min<int64_t>(8, tiles / kResidentWgs)));
+    p.row_tiles = (int)((rows + 32 * p.run_groups - 1) / (32 * p.run_groups));
+    p.nsplits = 1;
+    p.whole = (int)(batch * kv_heads * p.row_tiles);
   } else {
     const int64_t tiles = batch * kv_heads * p.row_tiles, slots = 256;  // one workgroup a compute unit
     const int64_t rest = tiles % slots;
@@ -961,15 +1134,19 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   a.chunks = p.chunks;
   a.whole = p.whole;
   a.split_tiles = p.split_tiles;
+  a.run_groups = p.run_groups;
   a.row_tiles = p.row_tiles;
   void* kargs[] = {&a};
   int64_t grid = a.whole + (int64_t)a.split_tiles * a.nsplits;
   if (p.few) grid = ((int64_t)a.batch * a.row_tiles * a.nsplits + 7) / 8 * 8 * (a.kv_heads / p.wg_heads);
   const hipError_t e =
-      hipLaunchKernel(!p.few            ? rows_kernel(a.head_dim)
+      hipLaunchKernel(p.run_groups      ? resident_kernel(a.head_dim)
+                      : !p.few          ? rows_kernel(a.head_dim)
                       : p.wg_heads == 2 ? tokens_kernel<2>(a.head_dim)
                                         : tokens_kernel<1>(a.head_dim),
-                      dim3((unsigned)grid), dim3(64 * (p.few ? kTokenWaves : kRowsWaves)), kargs, 0, stream);
+                      dim3((unsigned)grid),
+                      dim3(64 * (p.run_groups ? resident_waves(a.head_dim) : p.few ? kTokenWaves : kRowsWaves)), kargs, 0,
+                      stream);
   if (e != hipSuccess || a.nsplits == 1) return e;
   int slices = 1;
   while (slices < 16 && slices < a.nsplits) slices *= 2;
