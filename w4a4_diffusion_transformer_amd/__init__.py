@@ -295,26 +295,40 @@ def kq_tune_reset() -> None:
 # The entry points below take strided rows, tables and several optional tensors: their tensors are checked
 # against one another here (the C ABI sees only addresses), have to be on one device, and run on that device.
 
-def _rows(t, what: str, width: int, rows: int):
-    """Address and row stride of a bf16 matrix [rows, width] whose rows are contiguous."""
+def _wrong_place(t, what: str, dev: int):
     if not t.is_cuda:
         raise ValueError(f"{what}: tensor must be on the GPU")
+    raise ValueError(f"{what}: tensor on {t.device}, others on cuda:{dev}")
+
+
+def _device(t, what: str) -> int:
+    """Index of the GPU that a tensor is on."""
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{what}: tensor must be on the GPU")
+    return dev
+
+
+def _rows(t, what: str, width: int, rows: int, dev: int):
+    """Address and row stride of a bf16 matrix [rows, width] on GPU `dev` whose rows are contiguous."""
+    if t.get_device() != dev:
+        _wrong_place(t, what, dev)
     if t.dtype not in _BF16:
         raise TypeError(f"{what}: dtype {t.dtype} not in {_BF16}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+    if t.shape != (rows, width):
         raise ValueError(f"{what}: expected [{rows}, {width}], got {list(t.shape)}")
-    stride = t.stride()
-    if stride[1] != 1 and width > 1:
+    stride, step = t.stride()
+    if step != 1 and width > 1:
         raise ValueError(f"{what}: rows must be contiguous")
-    return t.data_ptr(), stride[0] if rows > 1 else width
+    return t.data_ptr(), stride if rows > 1 else width
 
 
-def _full(t, what: str, dtype, shape):
-    """Address of a contiguous tensor of this type and shape (None stays None)."""
+def _full(t, what: str, dtype, shape, dev: int):
+    """Address of a contiguous tensor of this type and shape on GPU `dev` (None stays None)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError(f"{what}: tensor must be on the GPU")
+    if t.get_device() != dev:
+        _wrong_place(t, what, dev)
     if t.dtype not in dtype:
         raise TypeError(f"{what}: dtype {t.dtype} not in {dtype}")
     if t.shape != shape or not t.is_contiguous():
@@ -322,17 +336,9 @@ def _full(t, what: str, dtype, shape):
     return t.data_ptr()
 
 
-def _one_device(first, *others) -> int:
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    return dev
-
-
 def _call(fn, where: str, dev: int, stream, *args):
-    """fn(*args, stream) on device `dev`: its current stream, or the one given."""
-    if dev != torch.cuda.current_device():
+    """fn(*args, stream) on GPU `dev` (its tensors are there): that GPU's current stream, or the one given."""
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _call(fn, where, dev, stream, *args)
     status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
@@ -355,14 +361,14 @@ def kq_gemm_mx_ex(a_codes, a_scales, b_codes, b_scales, bias=None, act: int = KQ
     rps = M if rows_per_sample is None else int(rows_per_sample)
     if gate is not None and rps <= 0 < M:
         raise ValueError("rows_per_sample must be positive")
-    dev = _one_device(a_codes, a_scales, b_codes, b_scales, bias, gate, residual, y_f32, y_bf16)
+    dev = _device(a_codes, "a_codes")
     _call(lib().kq_gemm_mx_ex, "kq_gemm_mx_ex", dev, stream,
-          _full(a_codes, "a_codes", _U8, (M, half)), _full(a_scales, "a_scales", _U8, (M, K // 32)), M,
-          _full(b_codes, "b_codes", _U8, (N, half)), _full(b_scales, "b_scales", _U8, (N, K // 32)), N, K,
-          _full(bias, "bias", _F32, (N,)), int(act),
-          None if gate is None else _full(gate, "gate", _F32, (-(-M // rps) if M else gate.shape[0], N)), rps or 1,
-          _full(residual, "residual", _BF16, (M, N)), _full(y_f32, "y_f32", _F32, (M, N)),
-          _full(y_bf16, "y_bf16", _BF16, (M, N)))
+          _full(a_codes, "a_codes", _U8, (M, half), dev), _full(a_scales, "a_scales", _U8, (M, K // 32), dev), M,
+          _full(b_codes, "b_codes", _U8, (N, half), dev), _full(b_scales, "b_scales", _U8, (N, K // 32), dev), N, K,
+          _full(bias, "bias", _F32, (N,), dev), act,
+          None if gate is None else _full(gate, "gate", _F32, (-(-M // rps) if M else gate.shape[0], N), dev), rps or 1,
+          _full(residual, "residual", _BF16, (M, N), dev), _full(y_f32, "y_f32", _F32, (M, N), dev),
+          _full(y_bf16, "y_bf16", _BF16, (M, N), dev))
     return y_f32, y_bf16
 
 
@@ -373,30 +379,29 @@ def alloc_cache(n_slots: int, width: int, device="cuda"):
     return zeros(width // 2), zeros(width // 32), zeros(width // 2), zeros(width // 32)
 
 
-def _cache(k_codes, k_scales, v_codes, v_scales, width: int, both: bool = True):
+def _cache(k_codes, k_scales, v_codes, v_scales, width: int, dev: int, both: bool = True):
     """(n_slots, four addresses) of a cache's pools; the values' are None without `both`."""
     n = k_codes.shape[0]
     codes, scales = (n, width // 2), (n, width // 32)
-    if both:
-        v = (_full(v_codes, "v_codes", _U8, codes), _full(v_scales, "v_scales", _U8, scales))
-    else:
-        v = (None, None)
-    return n, (_full(k_codes, "k_codes", _U8, codes), _full(k_scales, "k_scales", _U8, scales)) + v
+    k, ks = _full(k_codes, "k_codes", _U8, codes, dev), _full(k_scales, "k_scales", _U8, scales, dev)
+    if not both:
+        return n, (k, ks, None, None)
+    return n, (k, ks, _full(v_codes, "v_codes", _U8, codes, dev), _full(v_scales, "v_scales", _U8, scales, dev))
 
 
-def _cache_rows(K, V, slots):
+def _cache_rows(K, V, slots, dev: int):
     T, W = K.shape
-    k, ks = _rows(K, "K", W, T)
-    v, vs = (None, W) if V is None else _rows(V, "V", W, T)
-    return T, W, k, ks, v, vs, _full(slots, "slots", _I32, (T,))
+    k, ks = _rows(K, "K", W, T, dev)
+    v, vs = (None, W) if V is None else _rows(V, "V", W, T, dev)
+    return T, W, k, ks, v, vs, _full(slots, "slots", _I32, (T,), dev)
 
 
 def kq_cache_write(K, V, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
     """Quantize rows of K and V (bfloat16 [tokens, width], V may be None) to MXFP4 and write them to their slots
     (int32 [tokens], outside the cache: not written)."""
-    T, W, k, ks, v, vs, at = _cache_rows(K, V, slots)
-    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, W, V is not None)
-    dev = _one_device(K, V, slots, k_codes, k_scales, v_codes, v_scales)
+    dev = _device(K, "K")
+    T, W, k, ks, v, vs, at = _cache_rows(K, V, slots, dev)
+    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, W, dev, V is not None)
     _call(lib().kq_cache_write, "kq_cache_write", dev, stream, k, ks, v, vs, T, W, at, n, *pools)
     return k_codes, k_scales, v_codes, v_scales
 
@@ -404,9 +409,9 @@ def kq_cache_write(K, V, slots, k_codes, k_scales, v_codes, v_scales, stream=Non
 def kq_cache_read(k_codes, k_scales, v_codes, v_scales, slots, K, V, stream=None):
     """The values of slots (int32 [tokens], outside the cache: zeros) into K and V (bfloat16 [tokens, width], V may
     be None)."""
-    T, W, k, ks, v, vs, at = _cache_rows(K, V, slots)
-    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, W, V is not None)
-    dev = _one_device(K, V, slots, k_codes, k_scales, v_codes, v_scales)
+    dev = _device(K, "K")
+    T, W, k, ks, v, vs, at = _cache_rows(K, V, slots, dev)
+    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, W, dev, V is not None)
     _call(lib().kq_cache_read, "kq_cache_read", dev, stream, *pools, n, W, at, T, k, ks, v, vs)
     return K, V
 
@@ -434,7 +439,8 @@ def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_head
     dim = width // q_heads
     if width != q_heads * dim:
         raise ValueError(f"Q: {width} columns are not {q_heads} heads")
-    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, kv_heads * dim)
+    dev = _device(Q, "Q")
+    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, kv_heads * dim, dev)
     if page_table is not None:
         pages_per_seq = page_table.shape[1]
         if page_size is None:
@@ -445,23 +451,21 @@ def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_head
         pages_per_seq = n // page_size // max(1, batch)
     if max_q is None:
         max_q = rows // max(1, batch) if q_start is None else rows
-    dev = _one_device(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, page_table, q_start, lse, workspace)
-    q, qs = _rows(Q, "Q", width, rows)
-    o, os_ = _rows(out, "out", width, rows)
+    q, qs = _rows(Q, "Q", width, rows, dev)
+    o, os_ = _rows(out, "out", width, rows, dev)
     need = kq_attention_mx_workspace(rows, batch, max_q, q_heads, kv_heads, dim, pages_per_seq * page_size)
     if workspace is None and need:
         if stream is None:
-            with torch.cuda.device(dev):
-                workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
         else:  # memory of the stream that uses it, so that its reuse waits for this call
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
             with torch.cuda.stream(s):
                 workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
     wbytes = 0 if workspace is None else workspace.numel()
     _call(lib().kq_attention_mx, "kq_attention_mx", dev, stream, q, qs, rows,
-          _full(q_start, "q_start", _I32, (batch + 1,)), batch, max_q, *pools, n,
-          _full(page_table, "page_table", _I32, (batch, pages_per_seq)), pages_per_seq, page_size,
-          _full(kv_len, "kv_len", _I32, (batch,)), q_heads, kv_heads, dim, dim ** -0.5 if scale is None else scale,
-          int(causal), o, os_, _full(lse, "lse", _F32, (rows, q_heads)),
-          _full(workspace, "workspace", _U8, (wbytes,)), wbytes)
+          _full(q_start, "q_start", _I32, (batch + 1,), dev), batch, max_q, *pools, n,
+          _full(page_table, "page_table", _I32, (batch, pages_per_seq), dev), pages_per_seq, page_size,
+          _full(kv_len, "kv_len", _I32, (batch,), dev), q_heads, kv_heads, dim, dim ** -0.5 if scale is None else scale,
+          causal, o, os_, _full(lse, "lse", _F32, (rows, q_heads), dev),
+          _full(workspace, "workspace", _U8, (wbytes,), dev), wbytes)
     return out, lse
