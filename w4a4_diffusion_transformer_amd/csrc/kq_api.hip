@@ -349,8 +349,11 @@ kq_status run_cache(bool write, const uint16_t* k, int64_t k_stride, const uint1
   return from_hip(kq::launch_cache(write, v != nullptr, a, stream));
 }
 
-// Rows up to which kq_gemm_mx_ex takes the few-row form.
-constexpr int64_t kFewRows = 64;
+// Whether kq_gemm_mx_ex takes the few-row form: its time goes with the outputs, as the tile form's does not while its
+// tiles fit the GPU at once, and with K as the tile form's.  Measured around the limit, few-row against tiles (us):
+// 256 x 4608 x 1152 9.7 and 12.1, 256 x 6912 x 1152 14.0 and 12.5, 128 x 9216 x 2240 16.2 and 18.9, 256 x 9216 x 2240
+// 25.5 and 19.6, 1024 x 1152 x 4608 24.1 and 26.0, 1024 x 2240 x 5600 45.9 and 38.1, 256 x 4608 x 12288 52 and 58.
+bool few_rows(int64_t M, int64_t N) { return M * N <= (int64_t(5) << 18); }
 
 // Shared body of kq_gemm_mx (no epilogue) and kq_gemm_mx_ex.
 kq_status run_gemm(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, const uint8_t* B_codes,
@@ -380,7 +383,7 @@ kq_status run_gemm(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, c
   kq::GemmArgs g{A_codes, A_scales, B_codes, B_scales, (int)M, (int)N, (int)K, Y_f32, Y_bf16, e};
   // K = 32: a row has one scale byte, and the tile kernel's 4-byte scale reads of the last rows but one would
   // cross the end of the tensor (kq_gemm.hip patches the last row only, which is enough from K = 64 on)
-  if (K == 32 || (e.on && M <= kFewRows)) return from_hip(kq::launch_gemm_rows(g, stream));
+  if (K == 32 || (e.on && few_rows(M, N))) return from_hip(kq::launch_gemm_rows(g, stream));
   return from_hip(kq::launch_gemm(g, stream));
 }
 

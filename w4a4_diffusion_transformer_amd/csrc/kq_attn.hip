@@ -62,12 +62,6 @@ __device__ __forceinline__ float quarter_sum(float v) {
   return swap_sum32(__uint_as_float(s[0]) + __uint_as_float(s[1]));
 }
 
-// Orders a wave's own LDS accesses for the compiler; the hardware runs them in order.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // What one sequence and key head is to a workgroup.
 struct Seq {
   int64_t row0;  // first row of its queries in q, out and lse

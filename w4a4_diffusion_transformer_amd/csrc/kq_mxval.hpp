@@ -1,5 +1,5 @@
-// Reading MXFP4 on the device: values of codes, and the index arithmetic of
-// paged caches (gfx950 only).
+// Reading MXFP4 on the device: values of codes, the index arithmetic of paged
+// caches, and wave-private LDS (gfx950 only).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -29,6 +29,12 @@ __device__ __forceinline__ mx_bf16x8 mx_values8(unsigned word, unsigned byte) {
 // so n m / 2^(31 + l) exceeds n / d by n e / (d 2^(31 + l)) < 1 / d: the floors agree.
 __device__ __forceinline__ unsigned fast_div(unsigned n, Divisor d) {
   return (unsigned)(((uint64_t)n * d.m) >> d.shift);
+}
+
+// Orders a wave's own LDS accesses for the compiler; the hardware runs them in order.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 }  // namespace kq
