@@ -104,6 +104,8 @@ def test_binding_refuses_what_does_not_fit():
         kq.kq_attention_mx(x, *pools, at, x, 2, 2)
     with pytest.raises(ValueError):  # 64 columns are not 3 heads
         kq.kq_attention_mx(x, *pools, at, x, 3, 3)
+    with pytest.raises(ValueError):
+        kq.kq_attention_mx(x, *pools, at, x, 0, 1)
     with pytest.raises(ValueError):  # a table without its page size
         kq.kq_attention_mx(x, *pools, at, x, 2, 2, page_table=at.reshape(4, 1))
 

@@ -243,3 +243,17 @@ def test_cache_past_4_gib():
         small = [t[at].cpu() for t in cache]  # the same keys in order
         ref.check_attention(out, lse, ref.attention(q, small, lens, torch.zeros((1, 1), dtype=torch.int32), 250, 32, 32,
                                                     [0, q_len]))
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_a_cache_without_room(q_len):
+    """No pages to a sequence, or none in the cache that is whole: every query is empty."""
+    q = ref.bf16((2 * q_len, 128), 1).to(DEV)
+    lens = torch.tensor([5, 10 ** 6], dtype=torch.int32, device=DEV)
+    for per, n_slots in ((0, 64), (3, 15)):
+        cache = [torch.full((n_slots, w), 0xFF, dtype=torch.uint8, device=DEV) for w in (32, 2, 32, 2)]
+        table = torch.zeros((2, per), dtype=torch.int32, device=DEV)
+        out = torch.full((2 * q_len, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.zeros((2 * q_len, 2), device=DEV)
+        kq.kq_attention_mx(q, *cache, lens, out, 2, 1, page_size=16, page_table=table, lse=lse)
+        assert not out.any() and torch.isneginf(lse).all()

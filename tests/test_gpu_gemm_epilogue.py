@@ -45,7 +45,9 @@ def run(ops, bias, name, gate, rps, residual, fp32=True, bf16=True, in_place=Fal
 
 SIZES = [(1, 1, 32), (1, 6912, 1152), (2, 100, 5600), (7, 33, 96), (16, 640, 2240), (17, 257, 160), (32, 64, 12288),
          (33, 130, 1504), (64, 1152, 1152), (100, 300, 320), (129, 45, 64), (300, 257, 2240), (512, 384, 1152),
-         (1000, 520, 96)]
+         (1000, 520, 96),
+         # past the few-row form: half tiles, rows of any alignment, 192-row tiles, whole tiles and halves
+         (1400, 1000, 96), (1201, 1101, 160), (2500, 600, 2240), (3333, 2600, 96), (3333, 2601, 1504), (4352, 4096, 128)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
@@ -59,12 +61,12 @@ def test_everything_at_every_size(m, n, k):
     assert torch.equal(yb, y.to(torch.bfloat16))  # the same value, rounded once
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 70, 96), (40, 70, 96), (300, 70, 96)])
+@pytest.mark.parametrize("m,n,k", [(3, 70, 96), (40, 70, 96), (300, 70, 96), (1300, 1040, 64)])
 @pytest.mark.parametrize("name", list(ACTS))
 @pytest.mark.parametrize("parts", ["", "b", "g", "r", "bg", "gr", "br"])
 def test_each_part_alone(m, n, k, name, parts):
     ops = operands(m, n, k, 3)
-    rps = 7
+    rps = 7 if m < 1000 else 500
     bias, gate, residual = extras(m, n, rps, 4)
     bias, gate, residual = bias if "b" in parts else None, gate if "g" in parts else None, residual if "r" in parts else None
     want, tol = ref.gemm(*ops, bias, name, gate, rps, residual)
@@ -73,7 +75,7 @@ def test_each_part_alone(m, n, k, name, parts):
     assert torch.equal(yb, y.to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("m", [1, 20, 48, 300])
+@pytest.mark.parametrize("m", [1, 20, 48, 300, 9001])
 def test_residual_in_place(m):
     ops = operands(m, 150, 128, 5)
     bias, gate, residual = extras(m, 150, m, 6)
@@ -82,7 +84,7 @@ def test_residual_in_place(m):
     assert torch.equal(apart, same)
 
 
-@pytest.mark.parametrize("m", [2, 30, 260])
+@pytest.mark.parametrize("m", [2, 30, 260, 21000])
 def test_activation_tails(m):
     """Biases that reach far into both tails of each activation; results stay finite and exact to the bound."""
     ops = operands(m, 64, 32, 9)
@@ -103,10 +105,26 @@ def test_plain_product_of_one_block(m, n):
     assert ((y.cpu().double() - want).abs() <= tol).all()
 
 
-def test_same_sums_as_the_plain_product():
+@pytest.mark.parametrize("m,n", [(1100, 1300), (3333, 2600)])
+def test_same_sums_as_the_plain_product(m, n):
     """Above the sizes of the few-row form, without any part, the bits are kq_gemm_mx's."""
-    ops = [t.to(DEV) for t in operands(1100, 700, 2240, 10)]
-    a, b = (torch.empty((1100, 700), device=DEV) for _ in range(2))
+    ops = [t.to(DEV) for t in operands(m, n, 2240, 10)]
+    a, b = (torch.empty((m, n), device=DEV) for _ in range(2))
     kq.kq_gemm_mx(*ops, y_f32=a)
     kq.kq_gemm_mx_ex(*ops, y_f32=b)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,n", [(40, 72), (1400, 1000)])
+def test_outputs_and_residuals_that_start_anywhere(m, n):
+    """Rows of a whole number of 16-byte pieces whose matrices do not start at one: element accesses."""
+    ops = operands(m, n, 64, 12)
+    bias, gate, residual = extras(m, n, m, 13)
+    want, tol = ref.gemm(*ops, bias, "silu", gate, m, residual)
+    res = torch.empty(m * n + 1, dtype=torch.bfloat16, device=DEV)[1:].view(m, n)
+    res.copy_(residual)
+    flat = torch.full((m * n + 2,), 7.0, device=DEV)
+    y = flat[1:-1].view(m, n)
+    kq.kq_gemm_mx_ex(*[t.to(DEV) for t in ops], bias=bias.to(DEV), act=ACTS["silu"], gate=gate.to(DEV), residual=res, y_f32=y)
+    assert ((y.cpu().double() - want).abs() <= tol).all()
+    assert flat[0] == 7 and flat[-1] == 7

@@ -436,9 +436,9 @@ def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_head
     head_dim ** -0.5.  workspace (uint8, kq_attention_mx_workspace bytes) is allocated for the call if None."""
     rows, width = Q.shape
     batch = kv_len.shape[0]
-    dim = width // q_heads
-    if width != q_heads * dim:
+    if q_heads < 1 or width % q_heads:
         raise ValueError(f"Q: {width} columns are not {q_heads} heads")
+    dim = width // q_heads
     dev = _device(Q, "Q")
     n, pools = _cache(k_codes, k_scales, v_codes, v_scales, kv_heads * dim, dev)
     if page_table is not None:

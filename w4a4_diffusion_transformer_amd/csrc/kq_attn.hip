@@ -1121,6 +1121,7 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   a.by_page = make_divisor((unsigned)a.page_size);
   a.by_group = make_divisor((unsigned)a.group);
   a.capacity = a.n_pages > 0 ? a.pages_per_seq * a.page_size : 0;
+  if (a.pages_per_seq == 0) a.table = nullptr;  // no entry that page_entry could read
   a.c = a.scale * kLog2e;
   const AttnPlan p =
       attn_plan(a.batch, a.max_q, a.q_heads, a.kv_heads, a.head_dim, (int64_t)a.pages_per_seq * a.page_size);
