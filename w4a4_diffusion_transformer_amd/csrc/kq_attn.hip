@@ -298,13 +298,34 @@ __device__ __forceinline__ void attend_tile(const uint16_t* ks, const bf16x8 (&q
     for (int x = 0; x < 16; ++x) s[k][x] = 0.0f;
   // the wave in its products goes before the one in its softmax on the same SIMD: 1-3%
   __builtin_amdgcn_s_setprio(1);
+  // fragments two steps ahead of their products; at 64 channels and less the registers of four waves a
+  // SIMD are worth more (329 us against 383 for 2 x 4096 rows of 32 heads over 4096 keys)
+  constexpr int ND = DP / 16, kAhead = DP >= 96 ? 2 : 1;
+  bf16x8 kf[kAhead][2];
+  auto read_keys = [&](int d) {
 #pragma unroll
-  for (int d = 0; d < DP / 16; ++d)
+    for (int k = 0; k < 2; ++k)
+      kf[d % kAhead][k] = *reinterpret_cast<const bf16x8*>(&ks[(32 * k + col) * KS + 16 * d + 8 * half]);
+  };
+  if constexpr (kAhead > 1) {
+    read_keys(0);
+    read_keys(1);
+  }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&ks[(32 * k + col) * KS + 16 * d + 8 * half]);
-      s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[d], s[k], 0, 0, 0);
+  for (int d = 0; d < ND; ++d) {
+    if constexpr (kAhead == 1) {
+      read_keys(d);
+    } else {
+      __builtin_amdgcn_sched_barrier(0);
     }
+    const bf16x8 now[2] = {kf[d % kAhead][0], kf[d % kAhead][1]};
+    if constexpr (kAhead > 1) {
+      if (d + kAhead < ND) read_keys(d + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now[k], qf[d], s[k], 0, 0, 0);
+  }
   // a hole: some key under the highest that is there, or under the last that a query sees, is not
   const bool holes = (seen & (seen + 1)) != 0 || (seen != ~(uint64_t)0 && upto_max >= key + __builtin_popcountll(seen));
   if (holes || upto_min < key + kKeys - 1) mask_scores<2>(s, seen, holes, upto - key, half);
@@ -487,7 +508,15 @@ void attn_resident_kernel(AttnArgs a) {
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const RowsWork w = rows_work(a, blockIdx.x);
+  // XCD i has every head of the row tiles i, i + 8, ...: heads next to each other share cache lines of the
+  // codes and, where their rows are not whole lines, of the queries and the outputs
+  int id = blockIdx.x;
+  if (a.xcd_units) {
+    const int unit = id / (8 * a.kv_heads) * 8 + (id & 7);
+    if (unit >= a.xcd_units) return;
+    id = unit * a.kv_heads + (id >> 3) % a.kv_heads;
+  }
+  const RowsWork w = rows_work(a, id);
   const Seq sq = sequence(a, w.b);
   const int rows = min(sq.nq, a.max_q) * a.group;
   const int r0 = w.tile * 32 * a.run_groups;
@@ -1066,8 +1095,6 @@ const void* tokens_kernel(int d) {
 
 }  // namespace
 
-constexpr int64_t kResidentWgs = 384;
-
 // Few rows: up to two 16-row tiles for each sequence and key head.  Their
 // workgroups take four key heads where that leaves enough of them (the four
 // read the same cache lines together), else one, so that a short context is
@@ -1094,12 +1121,24 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
     if (steps < 4) p.nsplits = 1;
     p.chunks = (int)(std::max<int64_t>(1, each) * batch);
   } else if (capacity <= kKeys * resident_tiles((int)head_dim)) {
-    // runs of 256 rows, several where that leaves some three workgroups for each compute unit
-    const int64_t waves = resident_waves((int)head_dim), tiles = batch * kv_heads * ((rows + 32 * waves - 1) / (32 * waves));
-    p.run_groups = (int)(waves * std::max<int64_t>(1, std::min<int64_t>(8, tiles / kResidentWgs)));
-    p.row_tiles = (int)((rows + 32 * p.run_groups - 1) / (32 * p.run_groups));
+    // One workgroup fits a compute unit.  Of the row tiles that fill one to four rounds of workgroups, the
+    // number whose rounds take the least time, in units of what `waves` groups of 32 rows take together:
+    // kStage of it for the keys, and for a last part of the groups less than its share of the waves saves,
+    // since each then has more of its SIMD.  Against runs of `waves` groups, several where that leaves 384
+    // workgroups: 4 x 4096 rows of 16 heads of 96 over 300 keys 46.4 us and 62.2, 300 rows of one sequence
+    // 11.4 and 17.3, 2 x 4608 rows of 24 heads of 128 over 256 keys 47.6 and 52.6.
+    constexpr double kStage = 0.35, kAlone = 0.4;
+    const int64_t waves = resident_waves((int)head_dim), seqs = batch * kv_heads, groups = (rows + 31) / 32;
+    double least = 0;
+    for (int64_t round = (seqs + 255) / 256, end = round + 4; round < end; ++round) {
+      const int64_t n = std::max<int64_t>(1, std::min(groups, 256 * round / seqs)), each = (groups + n - 1) / n, rest = each % waves;
+      const double time = round * (kStage + each / waves + (rest ? kAlone + (1 - kAlone) * rest / waves : 0));
+      if (p.run_groups == 0 || time < least) p.run_groups = (int)each, least = time;
+    }
+    p.row_tiles = (int)((groups + p.run_groups - 1) / p.run_groups);
     p.nsplits = 1;
-    p.whole = (int)(batch * kv_heads * p.row_tiles);
+    p.whole = (int)(seqs * p.row_tiles);
+    if (batch * p.row_tiles % 8 == 0) p.xcd_units = (int)(batch * p.row_tiles);
   } else {
     const int64_t tiles = batch * kv_heads * p.row_tiles, slots = 256;  // one workgroup a compute unit
     const int64_t rest = tiles % slots;
@@ -1130,9 +1169,11 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   a.whole = p.whole;
   a.split_tiles = p.split_tiles;
   a.run_groups = p.run_groups;
+  a.xcd_units = p.xcd_units;
   a.row_tiles = p.row_tiles;
   void* kargs[] = {&a};
   int64_t grid = a.whole + (int64_t)a.split_tiles * a.nsplits;
+  if (a.xcd_units) grid = (int64_t)(a.xcd_units + 7) / 8 * 8 * a.kv_heads;
   if (p.few) grid = ((int64_t)a.batch * a.row_tiles * a.nsplits + 7) / 8 * 8 * (a.kv_heads / p.wg_heads);
   const hipError_t e =
       hipLaunchKernel(p.run_groups      ? resident_kernel(a.head_dim)

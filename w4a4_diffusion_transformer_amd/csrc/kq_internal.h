@@ -178,7 +178,7 @@ struct AttnArgs {
   float* part;  // workspace of a split launch
   // set by the launch
   Divisor by_page, by_group;
-  int capacity, group, row_tiles, nsplits, chunks, whole, split_tiles, run_groups;
+  int capacity, group, row_tiles, nsplits, chunks, whole, split_tiles, run_groups, xcd_units;
   float c;  // scale * log2(e)
 };
 
@@ -191,6 +191,7 @@ struct AttnPlan {
   int chunks;    // few: key ranges of the whole batch, for each group of heads
   int whole, split_tiles;  // many: tiles that are not divided, and the others
   int run_groups;          // many, with all keys in LDS: 32-row groups of a workgroup (its row tile); else 0
+  int xcd_units;           // of those: row tiles of which one XCD has every head; 0: dealt out singly
 };
 
 AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
