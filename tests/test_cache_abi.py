@@ -74,12 +74,20 @@ def test_attention_checks(lib):
     assert a(**big, ws=A, wb=need) == ALIAS
 
 
+def test_attention_of_no_sequences(lib):
+    """No batch is nothing to do and needs no workspace, at every division of the work."""
+    for rows, cap in ((1, 64), (1, 1 << 20), (4096, 64), (4096, 256), (4096, 1 << 20)):
+        assert lib.kq_attention_mx_workspace(rows, 0, rows, 4, 2, 64, cap) == 0
+        assert attention(lib, rows=rows, batch=0, max_q=rows, per=1, page=cap) == OK
+
+
 def test_gemm_ex_checks(lib):
     g = lambda a=A, m=4, n=8, k=64, bias=None, act=0, gate=None, rps=1, res=None, yf=None, yb=F: lib.kq_gemm_mx_ex(
         a, B, m, C, D, n, k, bias, act, gate, rps, res, yf, yb, None)
     assert g(act=4) == g(act=-1) == VARIANT
     assert g(k=48) == g(m=-1) == g(n=(1 << 22) + 1) == g(gate=E, rps=0) == g(gate=E, rps=-5) == SHAPE
     assert g(m=0) == g(n=0, gate=E) == OK
+    assert g(gate=F + 8, rps=(1 << 63) - 1) == ALIAS  # one sample
     assert g(yb=None) == g(a=None) == NULL
     assert g(bias=E + 2) == g(gate=E + 1) == g(res=E + 1) == ALIGN
     assert g(yb=B) == g(bias=F) == g(gate=F + 8) == g(res=F + 2) == g(yf=E, res=E) == g(yf=F) == ALIAS

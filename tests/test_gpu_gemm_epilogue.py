@@ -105,6 +105,18 @@ def test_plain_product_of_one_block(m, n):
     assert ((y.cpu().double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("m,n", [(1, 1), (257, 258), (258, 513), (1030, 1281), (1, 2000), (1400, 3)])
+def test_one_block_whose_last_rows_are_in_two_tiles(m, n):
+    """The same with the last three rows on both sides of a tile's end, and fewer rows than three."""
+    ops = operands(m, n, 32, 12)
+    want, tol = ref.gemm(*ops, None, "none", None, 1, None)
+    y, z = torch.empty((2, m, n), device=DEV)
+    ops = [t.to(DEV) for t in ops]
+    kq.kq_gemm_mx(*ops, y_f32=y)
+    kq.kq_gemm_mx_ex(*ops, y_f32=z)
+    assert ((y.cpu().double() - want).abs() <= tol).all() and ((z.cpu().double() - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("m,n", [(1100, 1300), (3333, 2600)])
 def test_same_sums_as_the_plain_product(m, n):
     """Above the sizes of the few-row form, without any part, the bits are kq_gemm_mx's."""

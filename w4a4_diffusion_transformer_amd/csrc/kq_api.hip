@@ -369,7 +369,8 @@ kq_status run_gemm(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, c
   const uint64_t mk = (uint64_t)M * (uint64_t)K, nk = (uint64_t)N * (uint64_t)K, mn = (uint64_t)M * (uint64_t)N;
   const Range outs[] = {{Y_f32, Y_f32 ? mn * 4 : 0}, {Y_bf16, Y_bf16 ? mn * 2 : 0}};
   // rows of a sample: at least M is one sample
-  if (e.gate) e.by_rows = kq::make_divisor((unsigned)std::min(rows_per_sample, M));
+  rows_per_sample = std::min(rows_per_sample, M);
+  if (e.gate) e.by_rows = kq::make_divisor((unsigned)rows_per_sample);
   const uint64_t samples = e.gate ? (uint64_t)((M + rows_per_sample - 1) / rows_per_sample) : 0;
   const bool in_place = e.residual && e.residual == Y_bf16;  // each element is read before it is written, by one lane
   const Range ins[] = {{A_codes, mk / 2},
@@ -381,9 +382,7 @@ kq_status run_gemm(const uint8_t* A_codes, const uint8_t* A_scales, int64_t M, c
                        {in_place ? nullptr : e.residual, mn * 2}};
   if (any_alias(outs, 2, ins, 7)) return KQ_ERR_ALIAS;
   kq::GemmArgs g{A_codes, A_scales, B_codes, B_scales, (int)M, (int)N, (int)K, Y_f32, Y_bf16, e};
-  // K = 32: a row has one scale byte, and the tile kernel's 4-byte scale reads of the last rows but one would
-  // cross the end of the tensor (kq_gemm.hip patches the last row only, which is enough from K = 64 on)
-  if (K == 32 || (e.on && few_rows(M, N))) return from_hip(kq::launch_gemm_rows(g, stream));
+  if (e.on && few_rows(M, N)) return from_hip(kq::launch_gemm_rows(g, stream));
   return from_hip(kq::launch_gemm(g, stream));
 }
 
@@ -609,6 +608,7 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
 int64_t kq_attention_mx_workspace(int64_t q_rows, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
                                   int64_t head_dim, int64_t capacity) {
   if (check_attention(q_rows, batch, max_q, q_heads, kv_heads, head_dim, capacity) != KQ_OK) return 0;
+  if (batch == 0 || max_q == 0) return 0;
   return kq::attn_workspace(q_rows, q_heads, head_dim,
                             kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity));
 }

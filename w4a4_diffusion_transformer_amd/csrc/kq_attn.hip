@@ -1115,7 +1115,7 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   p.row_tiles = (int)((rows + tile - 1) / tile);
   p.wg_heads = 1;
   if (p.few) {
-    const int64_t tiles = std::max<int64_t>(1, batch * kv_heads * p.row_tiles);
+    const int64_t tiles = batch * kv_heads * p.row_tiles;
     p.wg_heads = kv_heads % 2 == 0 && tiles * capacity >= kTwoHeadKeys ? 2 : 1;
     const int64_t wgs = tiles / p.wg_heads, unit = 64 / p.wg_heads * kTokenWaves;
     // Ranges of a sequence: up to one workgroup a compute unit as long as a wave has a tile, up to the two

@@ -210,7 +210,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
   // dword that crosses the end of a range reads as zero (range checks are
   // per dword: checked on MI355X), so when K / 32 is not a multiple of 4 the
   // final (K / 32) % 4 scale bytes of the last row of A and of B are read
-  // here with ordinary loads and patched in at the last stage.
+  // here with ordinary loads and patched in at the last stage.  At K = 32,
+  // one byte a row, the dwords of the last three rows cross the end: their
+  // bytes go to LDS before the stage loop.
   u32x4 da[NA], db[2], dsc;
   const int cchunk = (lane & 3) ^ ((lane >> 4) & 3);
 #pragma unroll
@@ -365,6 +367,16 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
   issue(0, 0, true, -1);
   issue(1, 1, false, -1);
   issue(2, 2, false, -1);
+  if (kblocks == 1) {  // uniform
+    const bool sa_side = wv < 4;
+    const int row = 64 * (wv & 3) + lane, at = (sa_side ? m0 : n0) + row, end = sa_side ? g.M : g.N;
+    __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's loads into the same places have landed
+    asm volatile("" ::: "memory");
+    if (row < (sa_side ? BM : kBN) && at < end && at >= end - 3)
+      (sa_side ? as_st[0] : bs_st[0])[16 * row] = (sa_side ? g.a_scales : g.b_scales)[at];
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);
+  }
   // loads issued after stage ks's: those of stages ks + 1 and ks + 2 (2 kOps
   // code loads), plus the scale load of stage ks + 1 or ks + 2 when one of
   // them opens a stage group (k = 3, 2)

@@ -1,6 +1,6 @@
 // W4A4 product for few rows: Y = deq(A) deq(B)^T with the epilogue, where the
 // 256 x 256 tiles of kq_gemm.hip would leave most of the GPU idle (a decode
-// batch, the modulation vectors of a guidance pair), and K = 32.
+// batch, the modulation vectors of a guidance pair).
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4, both operands E2M1: lane l holds 32
 // consecutive K values (16 bytes, one MX block) of row l % 16 at K offset

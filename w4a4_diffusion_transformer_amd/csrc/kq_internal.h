@@ -194,6 +194,7 @@ struct AttnPlan {
   int xcd_units;           // of those: row tiles of which one XCD has every head; 0: dealt out singly
 };
 
+// batch and max_q at least 1.
 AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                    int64_t capacity);
 int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, const AttnPlan& plan);
@@ -201,7 +202,7 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream);
 
 hipError_t launch_cache(bool write, bool both, const CacheArgs& args, hipStream_t stream);
 hipError_t launch_gemm(const GemmArgs& args, hipStream_t stream);
-// The same for few rows, or K = 32 (kq_gemm_rows.hip).
+// The same for few rows (kq_gemm_rows.hip).
 hipError_t launch_gemm_rows(const GemmArgs& args, hipStream_t stream);
 hipError_t launch_row_stats(const uint16_t* X, int T, int d, double eps, float* stats, hipStream_t stream);
 hipError_t launch_build(const float* P, int nb, float* K32, uint16_t* Kbf, int n_split, int inverse_t,
