@@ -432,7 +432,9 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
  * any number from 1 to 2^24.  Nothing of a slot that no key names is used,
  * whatever it holds.  causal != 0: with n queries and L keys, query i sees
  * keys j <= L - n + i (the queries are the sequence's last tokens), else all
- * L.  A query that sees no key gets out = 0 and lse = -infinity.
+ * L.  A query that sees no key gets out = 0 and lse = -infinity.  A value
+ * that is not finite (scale bytes above 252, which only tokens that were not
+ * finite get) may also reach queries of its sequence that do not see its key.
  *
  * head_dim is a multiple of 8 from 8 to 128, q_heads a multiple of kv_heads,
  * scale positive and finite.  lse (fp32 [q_rows][q_heads]) may be NULL.
@@ -440,8 +442,8 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
  * a second launch; the partial results need kq_attention_mx_workspace bytes
  * (0: none, workspace may be NULL), 16-byte aligned, free again when the call
  * has run: calls that may run at the same time, two captured graphs among
- * them, need one each.  The division depends on the sizes alone, so the same call gives
- * the same bits.  capacity = pages_per_seq * page_size.
+ * them, need one each.  The division depends on the sizes and the lengths
+ * alone, so the same call gives the same bits.  capacity = pages_per_seq * page_size.
  */
 int64_t kq_attention_mx_workspace(int64_t q_rows, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,
                                   int64_t head_dim, int64_t capacity);

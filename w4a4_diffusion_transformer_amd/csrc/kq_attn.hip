@@ -1119,13 +1119,13 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
     p.wg_heads = kv_heads % 2 == 0 && tiles * capacity >= kTwoHeadKeys ? 2 : 1;
     const int64_t wgs = tiles / p.wg_heads, unit = 64 / p.wg_heads * kTokenWaves;
     // Ranges of a sequence: up to one workgroup a compute unit as long as a wave has a tile, up to the two
-    // that fit while it has four; none below four tiles (the join costs as much: 512 keys of one sequence
-    // 7.9 us whole, 10.0 in two ranges; 4096 keys of eight sequences 20 us in four, 24 in eight).  Twice
-    // as many may be launched, for the longest sequences of a ragged batch.
+    // that fit while it has four; none below eight tiles a wave, where the join and its launch cost as much
+    // (1023 keys of one sequence 11.6 us whole, 11.4 in four ranges, called from Python 11.0 and 13.6; of 32
+    // sequences 14 whole, 20 in two; 2048 keys of one 19 whole, 11.5 in eight).  Twice as many may be
+    // launched, for the longest sequences of a ragged batch.
     const int64_t steps = capacity / unit;
-    const int64_t each = steps < 4 ? 1 : std::max(std::min(256 / wgs, steps), std::min(512 / wgs, steps / 4));
-    p.nsplits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * each, steps, 64}));
-    if (steps < 4) p.nsplits = 1;
+    const int64_t each = steps < 8 ? 1 : std::max(std::min(256 / wgs, steps), std::min(512 / wgs, steps / 4));
+    p.nsplits = steps < 8 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({2 * each, steps, 64}));
     p.chunks = (int)(std::max<int64_t>(1, each) * batch);
   } else if (capacity <= kKeys * resident_tiles((int)head_dim)) {
     // One workgroup fits a compute unit.  Of the row tiles that fill one to four rounds of workgroups, the
