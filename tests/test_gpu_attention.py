@@ -138,6 +138,14 @@ def test_uniform_batch_without_table_or_starts():
     ref.check_attention(out, lse, r)
 
 
+@pytest.mark.parametrize("dim,spare", [(40, 0), (64, 0), (128, 0), (64, 400), (72, 400), (128, 400)])
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_few_rows_over_divided_keys(dim, spare, q_len):
+    """A ragged batch whose key ranges are joined; with spare pages, room enough that a workgroup takes two heads."""
+    Case([q_len] * 6, [4600, 0, 2049, 1, 300, 3000], 8, 4, dim, 64 if spare == 0 else 128, seed=dim, spare=spare,
+         bad=[(0, 20, -1)]).check(causal=True)
+
+
 @pytest.mark.parametrize("q_len", [1, 140])
 def test_pages_outside_the_cache_are_masked(q_len):
     c = Case([q_len] * 3, [200, 64, 33], 4, 2, 64, 32, seed=7,
