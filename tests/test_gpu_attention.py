@@ -77,6 +77,12 @@ def test_head_widths(dim, q_len, kv):
     Case([q_len], [kv], 2 * kv_heads, kv_heads, dim, 16, seed=dim).check()
 
 
+@pytest.mark.parametrize("dim", [8, 32, 40, 64, 72, 96, 104, 128])
+def test_few_rows_over_some_hundreds_of_keys(dim):
+    """Key sets that are not divided, with every wave of a workgroup at work and with some idle; an empty one."""
+    Case([2, 2, 1, 2], [900, 260, 0, 129], 8, 4, dim, 48, seed=dim + 1, bad=[(0, 7, 10 ** 6)]).check(causal=True)
+
+
 @pytest.mark.parametrize("q_heads,kv_heads", [(1, 1), (3, 1), (8, 2), (32, 1), (5, 5), (48, 3)])
 @pytest.mark.parametrize("q_len", [1, 2, 37])
 def test_head_groups(q_heads, kv_heads, q_len):

@@ -604,7 +604,7 @@ void attn_resident_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------- few rows
 
-// A workgroup owns up to 16 rows of one or two key heads; its four waves take
+// A workgroup owns up to 16 rows of one or two key heads; its four (or eight) waves take
 // tiles of keys in turn (64 of one head, 32 of two), each with its own loads,
 // softmax and O, and join at the end.  What bounds it is reading the cache:
 //  - Every code is read once into registers, the next tile's while this one
@@ -627,7 +627,7 @@ void attn_resident_kernel(AttnArgs a) {
 // waits for another.  Key order within a 32-key step of the second product:
 // index j of quarter g is key 4 g + j (j < 4) or 16 + 4 g + j - 4, the order
 // S^T has.
-constexpr int kTokenRows = 16, kTokenWaves = 4;
+constexpr int kTokenRows = 16, kTokenWaves = 4, kWideWaves = 8;
 constexpr int64_t kTwoHeadKeys = int64_t(1) << 20;  // keys times heads from which a workgroup takes two heads
 
 // Keys of one workgroup of a sequence that sees `see`: the smallest share
@@ -665,15 +665,15 @@ __device__ __forceinline__ int token_share(const AttnArgs& a, int see, int unit,
   return (int)min(((int64_t)share + unit - 1) / unit * unit, (int64_t)1 << 30);
 }
 
-template <int DP, bool ALIGNED, int HEADS>
-__global__ __launch_bounds__(64 * kTokenWaves, 2) void attn_tokens_kernel(AttnArgs a) {
+template <int DP, bool ALIGNED, int HEADS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void attn_tokens_kernel(AttnArgs a) {
   constexpr int NS = DP / 32, NO = DP / 16, NB = ALIGNED ? 1 : NS;
   constexpr int KEYS = 64 / HEADS, KT = KEYS / 16;  // keys of a wave's tile, and in operand tiles of 16
   constexpr int LANES = 4 * HEADS, STEP = 64 / LANES;  // lanes that read one key, keys that one load reads
   constexpr int VS = HEADS * DP + 16, OS = DP + 4;     // LDS row strides: values (elements), outputs (floats)
-  constexpr int kVBytes = kTokenWaves * 32 * VS * 2, kOBytes = kTokenWaves * HEADS * kTokenRows * OS * 4;
+  constexpr int kVBytes = WAVES * 32 * VS * 2, kOBytes = WAVES * HEADS * kTokenRows * OS * 4;
   __shared__ __attribute__((aligned(16))) uint8_t shared[kVBytes > kOBytes ? kVBytes : kOBytes];
-  __shared__ float wave_m[kTokenWaves][HEADS][kTokenRows], wave_l[kTokenWaves][HEADS][kTokenRows];
+  __shared__ float wave_m[WAVES][HEADS][kTokenRows], wave_l[WAVES][HEADS][kTokenRows];
 
   const int tid = threadIdx.x, lane = tid & 63, quarter = lane >> 4, col = lane & 15;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -695,7 +695,7 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void attn_tokens_kernel(AttnAr
 
   const int last_q = (int)fast_div((unsigned)(min(r0 + kTokenRows, rows) - 1), a.by_group);
   const int see = a.causal ? max(0, min(sq.len, sq.len - sq.nq + last_q + 1)) : sq.len;
-  const int share = token_share(a, see, KEYS * kTokenWaves, lane);
+  const int share = token_share(a, see, KEYS * WAVES, lane);
   const int key0 = (int)min((int64_t)see, (int64_t)split * share), key1 = min(see, key0 + share);
 
   const int r = min(r0 + col, rows - 1);
@@ -887,7 +887,7 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void attn_tokens_kernel(AttnAr
   // tiles wv, wv + 4, ... of the range: the next tile's codes are in flight during this one's
   // product, and the slots of the one after, asked for before those codes (loads return in order:
   // behind them, waiting for a slot would wait for the codes too)
-  constexpr int kStep = KEYS * kTokenWaves;
+  constexpr int kStep = KEYS * WAVES;
   int key = key0 + KEYS * wv;
   if (key < key1) {
     Tile even, odd;
@@ -922,23 +922,23 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void attn_tokens_kernel(AttnAr
   for (int h = 0; h < HEADS; ++h) {
     float top = wave_m[0][h][col];
 #pragma unroll
-    for (int w = 1; w < kTokenWaves; ++w) top = fmaxf(top, wave_m[w][h][col]);
+    for (int w = 1; w < WAVES; ++w) top = fmaxf(top, wave_m[w][h][col]);
     const float mine = m[h] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m[h] - top) * a.c);
 #pragma unroll
     for (int d = 0; d < NO; ++d)
       *reinterpret_cast<f32x4*>(&os[((wv * HEADS + h) * kTokenRows + col) * OS + 16 * d + 4 * quarter]) = o[h][d] * mine;
   }
   __syncthreads();
-  for (int x = tid; x < HEADS * kTokenRows * nc; x += 64 * kTokenWaves) {
+  for (int x = tid; x < HEADS * kTokenRows * nc; x += 64 * WAVES) {
     const int hq = x / nc, ch = x - hq * nc, hw = hq / kTokenRows, q = hq % kTokenRows;
     if (r0 + q >= rows) continue;
     float best = wave_m[0][hw][q];
 #pragma unroll
-    for (int w = 1; w < kTokenWaves; ++w) best = fmaxf(best, wave_m[w][hw][q]);
+    for (int w = 1; w < WAVES; ++w) best = fmaxf(best, wave_m[w][hw][q]);
     float sum = 0.0f;
     f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kTokenWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       const float wm = wave_m[w][hw][q];
       sum += wm == -__builtin_inff() ? 0.0f : wave_l[w][hw][q] * __builtin_amdgcn_exp2f((wm - best) * a.c);
       const f32x4* src = reinterpret_cast<const f32x4*>(&os[((w * HEADS + hw) * kTokenRows + q) * OS + 8 * ch]);
@@ -1088,15 +1088,15 @@ const void* resident_kernel(int d) {
                    : (const void*)&attn_resident_kernel<128, false>;
 }
 
-template <int HEADS>
+template <int HEADS, int WAVES>
 const void* tokens_kernel(int d) {
-  if (d == 32) return (const void*)&attn_tokens_kernel<32, true, HEADS>;
-  if (d == 64) return (const void*)&attn_tokens_kernel<64, true, HEADS>;
-  if (d == 128) return (const void*)&attn_tokens_kernel<128, true, HEADS>;
-  return d < 32   ? (const void*)&attn_tokens_kernel<32, false, HEADS>
-         : d < 64 ? (const void*)&attn_tokens_kernel<64, false, HEADS>
-         : d <= 96 ? (const void*)&attn_tokens_kernel<96, false, HEADS>
-                   : (const void*)&attn_tokens_kernel<128, false, HEADS>;
+  if (d == 32) return (const void*)&attn_tokens_kernel<32, true, HEADS, WAVES>;
+  if (d == 64) return (const void*)&attn_tokens_kernel<64, true, HEADS, WAVES>;
+  if (d == 128) return (const void*)&attn_tokens_kernel<128, true, HEADS, WAVES>;
+  return d < 32   ? (const void*)&attn_tokens_kernel<32, false, HEADS, WAVES>
+         : d < 64 ? (const void*)&attn_tokens_kernel<64, false, HEADS, WAVES>
+         : d <= 96 ? (const void*)&attn_tokens_kernel<96, false, HEADS, WAVES>
+                   : (const void*)&attn_tokens_kernel<128, false, HEADS, WAVES>;
 }
 
 }  // namespace
@@ -1120,12 +1120,16 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
     const int64_t wgs = tiles / p.wg_heads, unit = 64 / p.wg_heads * kTokenWaves;
     // Ranges of a sequence: up to one workgroup a compute unit as long as a wave has a tile, up to the two
     // that fit while it has four; none below eight tiles a wave, where the join and its launch cost as much
-    // (1023 keys of one sequence 11.6 us whole, 11.4 in four ranges, called from Python 11.0 and 13.6; of 32
-    // sequences 14 whole, 20 in two; 2048 keys of one 19 whole, 11.5 in eight).  Twice as many may be
+    // (1023 keys of one sequence 10.6 us whole, 11.4 in four ranges, called from Python 9.7 and 13.6; of 32
+    // sequences 14 whole, 20 in two; 2048 keys of one 17 whole, 11.2 in eight).  Twice as many may be
     // launched, for the longest sequences of a ragged batch.
     const int64_t steps = capacity / unit;
     const int64_t each = steps < 8 ? 1 : std::max(std::min(256 / wgs, steps), std::min(512 / wgs, steps / 4));
     p.nsplits = steps < 8 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({2 * each, steps, 64}));
+    // Eight waves where that many keys are not divided and the GPU has room: 1023 keys of one sequence, 32 heads
+    // over 8, 10.6 us and 11.6 (called from Python 9.7 and 11.0); at a workgroup for every compute unit 32
+    // sequences take 14.6 and 14.3.
+    p.wide = p.nsplits == 1 && p.wg_heads == 1 && wgs <= 128 && capacity > 64 * kTokenWaves;
     p.chunks = (int)(std::max<int64_t>(1, each) * batch);
   } else if (capacity <= kKeys * resident_tiles((int)head_dim)) {
     // One workgroup fits a compute unit.  Of the row tiles that fill one to four rounds of workgroups, the
@@ -1185,10 +1189,11 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   const hipError_t e =
       hipLaunchKernel(p.run_groups      ? resident_kernel(a.head_dim)
                       : !p.few          ? rows_kernel(a.head_dim)
-                      : p.wg_heads == 2 ? tokens_kernel<2>(a.head_dim)
-                                        : tokens_kernel<1>(a.head_dim),
+                      : p.wg_heads == 2 ? tokens_kernel<2, kTokenWaves>(a.head_dim)
+                      : p.wide          ? tokens_kernel<1, kWideWaves>(a.head_dim)
+                                        : tokens_kernel<1, kTokenWaves>(a.head_dim),
                       dim3((unsigned)grid),
-                      dim3(64 * (p.run_groups ? resident_waves(a.head_dim) : p.few ? kTokenWaves : kRowsWaves)), kargs, 0,
+                      dim3(64 * (p.run_groups ? resident_waves(a.head_dim) : p.wide ? kWideWaves : p.few ? kTokenWaves : kRowsWaves)), kargs, 0,
                       stream);
   if (e != hipSuccess || a.nsplits == 1) return e;
   int slices = 1;

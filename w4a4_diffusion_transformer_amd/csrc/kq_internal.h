@@ -188,6 +188,7 @@ struct AttnPlan {
   bool few;
   int row_tiles, nsplits;
   int wg_heads;  // key heads of a workgroup
+  bool wide;     // few: workgroups of eight waves, not four
   int chunks;    // few: key ranges of the whole batch, for each group of heads
   int whole, split_tiles;  // many: tiles that are not divided, and the others
   int run_groups;          // many, with all keys in LDS: 32-row groups of a workgroup (its row tile); else 0
