@@ -621,7 +621,9 @@ void attn_resident_kernel(AttnArgs a) {
 //  - With two heads those reads are whole 128-byte lines: a compute unit has
 //    about as many requests in flight either way, so twice the bytes (75 us,
 //    3.9 TB/s; 256 sequences of 2048: 128 us, 4.5 TB/s, of the 5.1 to 5.9 that
-//    a plain read of as much reaches).
+//    a plain read of as much reaches).  Between 104 and 120 channels two
+//    heads' tiles do not fit the registers (36 spilled, 491 us against 412
+//    with one for 32 sequences of 8192 keys, 20 heads of 112).
 // Keys change lanes as codes through LDS, values as bf16 for their
 // transposition (32 keys at a time), both in wave-private memory, so no wave
 // waits for another.  Key order within a 32-key step of the second product:
@@ -1093,10 +1095,12 @@ const void* tokens_kernel(int d) {
   if (d == 32) return (const void*)&attn_tokens_kernel<32, true, HEADS, WAVES>;
   if (d == 64) return (const void*)&attn_tokens_kernel<64, true, HEADS, WAVES>;
   if (d == 128) return (const void*)&attn_tokens_kernel<128, true, HEADS, WAVES>;
-  return d < 32   ? (const void*)&attn_tokens_kernel<32, false, HEADS, WAVES>
-         : d < 64 ? (const void*)&attn_tokens_kernel<64, false, HEADS, WAVES>
-         : d <= 96 ? (const void*)&attn_tokens_kernel<96, false, HEADS, WAVES>
-                   : (const void*)&attn_tokens_kernel<128, false, HEADS, WAVES>;
+  if (d < 32) return (const void*)&attn_tokens_kernel<32, false, HEADS, WAVES>;
+  if (d < 64) return (const void*)&attn_tokens_kernel<64, false, HEADS, WAVES>;
+  // two heads of 104 to 120 channels do not fit the registers
+  if constexpr (HEADS == 1)
+    if (d > 96) return (const void*)&attn_tokens_kernel<128, false, HEADS, WAVES>;
+  return (const void*)&attn_tokens_kernel<96, false, HEADS, WAVES>;
 }
 
 }  // namespace
@@ -1116,7 +1120,7 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   p.wg_heads = 1;
   if (p.few) {
     const int64_t tiles = batch * kv_heads * p.row_tiles;
-    p.wg_heads = kv_heads % 2 == 0 && tiles * capacity >= kTwoHeadKeys ? 2 : 1;
+    p.wg_heads = kv_heads % 2 == 0 && (head_dim <= 96 || head_dim == 128) && tiles * capacity >= kTwoHeadKeys ? 2 : 1;
     const int64_t wgs = tiles / p.wg_heads, unit = 64 / p.wg_heads * kTokenWaves;
     // Ranges of a sequence: up to one workgroup a compute unit as long as a wave has a tile, up to the two
     // that fit while it has four; none below eight tiles a wave, where the join and its launch cost as much
