@@ -147,13 +147,13 @@ class Tokens:
         self.heads, self.kv_heads, dim, self.page, n = 8, 2, 128, 64, 3000
         W = self.kv_heads * dim
         self.q = ref.bf16((2, self.heads * dim), seed).to(DEV)
-        self.cache = kq.alloc_cache(2 * 48 * self.page, W, DEV)
+        self.cache = kq.alloc_cache(2 * 50 * self.page, W, DEV)
         slots = torch.arange(self.cache[0].shape[0], dtype=torch.int32, device=DEV)
         x = ref.bf16((slots.numel(), 2 * W), seed + 1).to(DEV)
         kq.kq_cache_write(x[:, :W], x[:, W:], slots, *self.cache)
         self.lens = torch.tensor([n, 700], dtype=torch.int32, device=DEV)
         self.out, self.lse = torch.empty_like(self.q), torch.empty((2, self.heads), device=DEV)
-        assert kq.kq_attention_mx_workspace(2, 2, 1, self.heads, self.kv_heads, dim, 48 * self.page) > 0
+        assert kq.kq_attention_mx_workspace(2, 2, 1, self.heads, self.kv_heads, dim, 50 * self.page) > 0
 
     def run(self, **kw):
         kq.kq_attention_mx(self.q, *self.cache, self.lens, self.out, self.heads, self.kv_heads, page_size=self.page,
@@ -221,6 +221,20 @@ def test_a_stream_that_is_not_the_current_one():
     assert all(same(t.outputs(), w) for t, w in zip(things, want))
 
 
+def test_the_default_stream_by_address():
+    """stream=0 is the default stream, also from inside another one."""
+    t = Tokens(25)
+    t.run()
+    torch.cuda.synchronize()
+    want = t.outputs()
+    t.out.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        t.run(stream=0)
+    torch.cuda.synchronize()
+    assert same(t.outputs(), want)
+
+
 def test_threads_on_their_own_streams():
     things = [Tokens(30), Block(31), Tokens(32), Block(33)]
     want = []
@@ -253,7 +267,7 @@ def test_a_workspace_of_ones_own():
     t.run()
     torch.cuda.synchronize()
     want = t.outputs()
-    need = kq.kq_attention_mx_workspace(2, 2, 1, 8, 2, 128, 48 * 64)
+    need = kq.kq_attention_mx_workspace(2, 2, 1, 8, 2, 128, 50 * 64)
     ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN wherever nothing was written
     t.run(workspace=ws)
     torch.cuda.synchronize()
