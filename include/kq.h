@@ -432,9 +432,11 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
  * any number from 1 to 2^24.  Nothing of a slot that no key names is used,
  * whatever it holds.  causal != 0: with n queries and L keys, query i sees
  * keys j <= L - n + i (the queries are the sequence's last tokens), else all
- * L.  A query that sees no key gets out = 0 and lse = -infinity.  A value
- * that is not finite (scale bytes above 252, which only tokens that were not
- * finite get) may also reach queries of its sequence that do not see its key.
+ * L.  A query that sees no key, or whose scores are all -infinity, gets out = 0
+ * and lse = -infinity; a NaN among the scores of a query makes its out and
+ * lse NaN.  A value that is not finite (scale bytes above 252, which only
+ * tokens that were not finite get) may also reach queries of its sequence
+ * that do not see its key.
  *
  * head_dim is a multiple of 8 from 8 to 128, q_heads a multiple of kv_heads,
  * scale positive and finite.  lse (fp32 [q_rows][q_heads]) may be NULL.

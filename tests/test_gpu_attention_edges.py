@@ -1,0 +1,60 @@
+"""kq_attention_mx on an MI355X where its ways of dividing the work meet values, batches and calls at their limits."""
+import pytest
+import torch
+
+import cache_reference as ref
+from test_gpu_attention import DEV, Case
+
+kq = pytest.importorskip("w4a4_diffusion_transformer_amd")
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    kq.lib()
+
+
+def workspace(c, q_len):
+    return kq.kq_attention_mx_workspace(c.rows, len(c.kv_len), max(q_len), c.heads, c.kv_heads, c.dim, c.per * c.page)
+
+
+# queries, keys, heads, key heads, channels, spare pages, whether key ranges are joined
+NAN_CASES = [([1, 1], [3000, 17], 8, 2, 128, 0, True),         # few rows, a head a workgroup
+             ([1, 1, 1], [4600, 2049, 300], 8, 4, 64, 4000, True),  # two heads a workgroup
+             ([2, 1], [3000, 900], 8, 4, 72, 4000, True),
+             ([3, 2], [100, 64], 4, 2, 64, 0, False),          # whole, four waves
+             ([2, 2], [900, 260], 8, 4, 40, 0, False),         # whole, eight
+             ([140, 30], [700, 600], 4, 2, 64, 0, True),       # many rows
+             ([140, 30], [100, 70], 4, 2, 64, 0, False)]       # many rows, keys on chip
+
+
+@pytest.mark.parametrize("q_len,kv,q_heads,kv_heads,dim,spare,joined", NAN_CASES)
+@pytest.mark.parametrize("causal", [False, True])
+def test_a_nan_query_gives_nan_and_stays_alone(q_len, kv, q_heads, kv_heads, dim, spare, joined, causal):
+    """out and lse of the query are NaN, however its keys are divided, and no other query's change."""
+    c = Case(q_len, kv, q_heads, kv_heads, dim, 64 if spare == 0 else 128, seed=61, spare=spare)
+    assert (workspace(c, q_len) > 0) == joined
+    r = [t.clone() for t in c.reference(causal=causal)]
+    row = q_len[0] - 1  # the first sequence's last query
+    c.q[row] = float("nan")
+    out, lse = c.run(causal=causal)
+    assert torch.isnan(out[row]).all() and torch.isnan(lse[row]).all()
+    lse[row], r[1][row] = 0.0, 0.0
+    r[4][row] = False
+    ref.check_attention(out, lse, r)
+
+
+@pytest.mark.parametrize("q_len,q_heads,kv_heads,dim,first,last,kv", [
+    ([1], 8, 2, 64, 64, 128, 130),      # all that one wave of a whole key set has
+    ([1], 8, 2, 128, 0, 3000, 3000),    # every key of a divided one
+    ([1], 8, 2, 128, 2990, 3000, 3000),
+    ([140], 4, 2, 64, 64, 128, 700), ([140], 4, 2, 64, 0, 64, 100)])
+def test_nan_keys_reach_every_query_that_sees_them(q_len, q_heads, kv_heads, dim, first, last, kv):
+    c = Case(q_len, [kv], q_heads, kv_heads, dim, 64, seed=62)
+    at = ref.slots_of(c.table, 0, kv, 64, c.cache[0].shape[0])[first:last]
+    c.cache[1][at] = 0xFF  # key scales that read as NaN
+    out, lse = c.run()
+    assert torch.isnan(out).all() and torch.isnan(lse).all()

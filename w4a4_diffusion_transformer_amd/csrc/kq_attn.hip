@@ -941,8 +941,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_tokens_kernel(AttnArgs a) 
     f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      const float wm = wave_m[w][hw][q];
-      sum += wm == -__builtin_inff() ? 0.0f : wave_l[w][hw][q] * __builtin_amdgcn_exp2f((wm - best) * a.c);
+      const float wm = wave_m[w][hw][q], wl = wave_l[w][hw][q];
+      // a wave that saw no key is known by its sum: one whose scores are all NaN keeps the maximum -inf too
+      sum += wl == 0.0f ? 0.0f : wl * __builtin_amdgcn_exp2f((wm - best) * a.c);
       const f32x4* src = reinterpret_cast<const f32x4*>(&os[((w * HEADS + hw) * kTokenRows + q) * OS + 8 * ch]);
       lo += src[0];
       hi += src[1];
