@@ -44,6 +44,19 @@ def test_cache_read_checks(lib):
     assert r(ks=128, vs=136, v=A + 128) == ALIAS
 
 
+def test_cache_read_into_columns_in_either_order(lib):
+    """K and V as column ranges of one matrix, V above or below K, at strides that are and are not powers of two."""
+    r = lambda k, v, w, s: lib.kq_cache_read(D, E, F, G, 16, w, C, 4, k, s, v, s, None)
+    for w, s in ((1152, 2304), (64, 136), (64, 128), (1024, 4096), (96, 200)):
+        base = A + 16 * s
+        # elements from one to the other, no row of them touching; the call gets as far as the launch, so only where
+        # that has no device to go to
+        for d in () if torch.cuda.is_available() else (w, s - w, 2 * s + w, -s + w):
+            assert r(base, base + 2 * d, w, s) == r(base + 2 * d, base, w, s) == HIP, (w, s, d)
+        for d in (0, 8, w - 8, s - w + 8, s, s + w - 8, 2 * s - 8):
+            assert r(base, base + 2 * d, w, s) == r(base + 2 * d, base, w, s) == ALIAS, (w, s, d)
+
+
 def attention(lib, q=A, qs=256, rows=8, start=None, batch=2, max_q=4, kc=B, ks=C, vc=D, vs=E, n=256, table=F, per=2,
               page=64, lens=G, hq=4, hk=2, dim=64, scale=0.125, causal=0, out=H, os_=256, lse=None, ws=None, wb=0):
     return lib.kq_attention_mx(q, qs, rows, start, batch, max_q, kc, ks, vc, vs, n, table, per, page, lens, hq, hk, dim,

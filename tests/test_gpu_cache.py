@@ -105,3 +105,18 @@ def test_no_tokens_and_no_slots():
         kq.kq_cache_write(x, x, at, *empty)
     torch.cuda.synchronize()
     assert all((t == 0xFF).all() for t in cache)
+
+
+@pytest.mark.parametrize("width", [32, 1152])
+def test_read_into_columns_with_the_values_first(width):
+    """One matrix whose first columns take V and whose last take K."""
+    cache = filled(9, width)
+    kv = ref.bf16((9, 2 * width), width)
+    at = torch.arange(9, dtype=torch.int32, device=DEV)
+    kq.kq_cache_write(kv[:, :width].contiguous().to(DEV), kv[:, width:].contiguous().to(DEV), at, *cache)
+    out = torch.full((9, 2 * width + 40), 7.0, dtype=torch.bfloat16, device=DEV)
+    kq.kq_cache_read(*cache, at, out[:, width + 40:], out[:, :width])
+    got = out.cpu()
+    assert torch.equal(got[:, width + 40:].double(), ref.values(*cache[:2]))
+    assert torch.equal(got[:, :width].double(), ref.values(*cache[2:]))
+    assert (got[:, width:width + 40] == 7).all()

@@ -300,7 +300,7 @@ bool good_stride(int64_t stride, int64_t width) {
 // Whether two row sets of the same count and width, at the same stride, interleave without touching (column
 // ranges of one matrix).
 bool columns_apart(const uint16_t* x, const uint16_t* y, int64_t stride, int64_t width) {
-  int64_t d = (int64_t)((reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) / 2) % stride;
+  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) / 2 % stride;  // y may lie below
   if (d < 0) d += stride;
   return d >= width && d + width <= stride;
 }
