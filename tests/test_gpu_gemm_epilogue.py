@@ -140,3 +140,21 @@ def test_outputs_and_residuals_that_start_anywhere(m, n):
     kq.kq_gemm_mx_ex(*[t.to(DEV) for t in ops], bias=bias.to(DEV), act=ACTS["silu"], gate=gate.to(DEV), residual=res, y_f32=y)
     assert ((y.cpu().double() - want).abs() <= tol).all()
     assert flat[0] == 7 and flat[-1] == 7
+
+
+# half tiles; 192-row tiles; whole tiles and halves; whole tiles of more rows than 192-row ones fit the GPU
+TILES = [(1100, 1300, 64), (3333, 2600, 96), (4352, 4096, 32), (5111, 2568, 512)]
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_every_row_and_channel_of_a_tile(m, n, k):
+    """The sums reach the epilogue through local memory, each wave's through a part of its own: with a bias the bits are
+    the plain product's, which stores from registers, and one fp32 addition's."""
+    ops = [t.to(DEV) for t in operands(m, n, k, 14)]
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(15)).to(DEV)
+    a = torch.empty((m, n), device=DEV)
+    y = torch.full((m, n), 7.0, device=DEV)
+    yb = torch.full((m, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    kq.kq_gemm_mx(*ops, y_f32=a)
+    kq.kq_gemm_mx_ex(*ops, bias=bias, y_f32=y, y_bf16=yb)
+    assert torch.equal(y, a + bias) and torch.equal(yb, (a + bias).to(torch.bfloat16))

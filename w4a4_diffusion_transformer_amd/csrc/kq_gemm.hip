@@ -108,7 +108,12 @@ __device__ __forceinline__ void lds_barrier() {
 // alone: 48).  Non-temporal stores: 2-7% faster than device scope or the default here.
 constexpr int kBandStride = 68;               // floats per row of a band: 64 and a pad against bank conflicts
 constexpr int kBandF = 32 * kBandStride;      // floats per wave
-static_assert(8 * kBandF * 4 <= kStages * kTileB * 2, "the bands fit the ring");
+
+// The stages' operand codes: A's and B's ring, one object, which the epilogue's bands use as one.
+struct Ring {
+  uint8_t a[kStages][kTileB], b[kStages][kTileB];
+};
+static_assert(8 * kBandF * 4 <= sizeof(Ring), "the bands fit the ring");
 
 template <int MI>
 __device__ __forceinline__ void store_epilogue(const GemmArgs& g, const f32x16 (&acc)[MI][2], int m0, int n0,
@@ -184,9 +189,10 @@ __device__ __forceinline__ void store_epilogue(const GemmArgs& g, const f32x16 (
 // whole 256 x 256 tile, MI = 2 half of one (see launch_gemm).  Each wave
 // computes 32 MI rows x 64 columns (MI x 2 MFMA tiles of 32 x 32).
 template <int MI, bool EPI>
-__device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uint8_t (&a_st)[kStages][kTileB],
-                                          uint8_t (&b_st)[kStages][kTileB], uint8_t (&as_st)[2][kScB],
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, Ring& ring, uint8_t (&as_st)[2][kScB],
                                           uint8_t (&bs_st)[2][kScB]) {
+  uint8_t(&a_st)[kStages][kTileB] = ring.a;
+  uint8_t(&b_st)[kStages][kTileB] = ring.b;
   constexpr int BM = 64 * MI;   // rows of the tile
   constexpr int NA = (MI + 1) / 2;  // 16-row groups of A each wave stages per stage (MI = 3: four lie past the tile, no rows)
   constexpr int kOps = NA + 2;  // code loads per wave and stage
@@ -406,7 +412,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
   // no faster.
   const int64_t N = g.N;
   if constexpr (EPI) {
-    store_epilogue<MI>(g, acc, m0, n0, mrows, wm, wn, lane, reinterpret_cast<float*>(&a_st[0][0]) + wv * kBandF);
+    store_epilogue<MI>(g, acc, m0, n0, mrows, wm, wn, lane, reinterpret_cast<float*>(&ring) + wv * kBandF);
     return;
   }
 #pragma unroll
@@ -454,8 +460,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int m0, int n0, uin
 // rows and B rows in its L2.
 template <bool EPI>
 __global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
-  __shared__ __attribute__((aligned(1024))) uint8_t a_st[kStages][kTileB];
-  __shared__ __attribute__((aligned(1024))) uint8_t b_st[kStages][kTileB];
+  __shared__ __attribute__((aligned(1024))) Ring ring;
   __shared__ __attribute__((aligned(256))) uint8_t as_st[2][kScB];  // by parity of the stage group
   __shared__ __attribute__((aligned(256))) uint8_t bs_st[2][kScB];
 
@@ -478,11 +483,11 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
   const int w = t - grp * per_group;
   const int tm = first + w % rows, tn = w / rows;
   if (EPI && g.tile_mi == 3)
-    gemm_tile<3, EPI>(g, tm * 192, tn * kBN, a_st, b_st, as_st, bs_st);
+    gemm_tile<3, EPI>(g, tm * 192, tn * kBN, ring, as_st, bs_st);
   else if (whole)
-    gemm_tile<4, EPI>(g, tm * kBM, tn * kBN, a_st, b_st, as_st, bs_st);
+    gemm_tile<4, EPI>(g, tm * kBM, tn * kBN, ring, as_st, bs_st);
   else
-    gemm_tile<2, EPI>(g, tm * kBM + 128 * half, tn * kBN, a_st, b_st, as_st, bs_st);
+    gemm_tile<2, EPI>(g, tm * kBM + 128 * half, tn * kBN, ring, as_st, bs_st);
 }
 
 }  // namespace
