@@ -158,3 +158,19 @@ def test_every_row_and_channel_of_a_tile(m, n, k):
     kq.kq_gemm_mx(*ops, y_f32=a)
     kq.kq_gemm_mx_ex(*ops, bias=bias, y_f32=y, y_bf16=yb)
     assert torch.equal(y, a + bias) and torch.equal(yb, (a + bias).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_bands_of_a_wave_follow_one_another(m, n, k):
+    """Every part of the epilogue, in place: each band of rows is read from local memory whole before the next one
+    takes its place.  Each part is one fp32 operation on the plain product, so the bits are torch's."""
+    ops = [t.to(DEV) for t in operands(m, n, k, 16)]
+    rps = m // 3
+    bias, gate, residual = (t.to(DEV) for t in extras(m, n, rps, 17))
+    a = torch.empty((m, n), device=DEV)
+    kq.kq_gemm_mx(*ops, y_f32=a)
+    want = (residual.float() + (a + bias) * gate.repeat_interleave(rps, 0)[:m]).to(torch.bfloat16)
+    for _ in range(3):
+        x = residual.clone()
+        kq.kq_gemm_mx_ex(*ops, bias=bias, gate=gate, rows_per_sample=rps, residual=x, y_bf16=x)
+        assert torch.equal(x, want)

@@ -152,6 +152,7 @@ __device__ __forceinline__ void store_epilogue(const GemmArgs& g, const f32x16 (
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) band[(8 * (r >> 2) + 4 * fh + (r & 3)) * kBandStride + 32 * j + fr] = acc[i][j][r];
+    wave_lds_fence();  // read by other lanes of the wave
     const int brows = min(32, max(0, mrows - r0));
     const auto yf = rsrc_uniform(g.y_f32 + (m0 + r0) * N, vec && g.y_f32 ? (int64_t)brows * N * 4 : 0);
     const auto yb = rsrc_uniform(g.y_bf16 + (m0 + r0) * N, vec && g.y_bf16 ? (int64_t)brows * N * 2 : 0);
@@ -182,6 +183,7 @@ __device__ __forceinline__ void store_epilogue(const GemmArgs& g, const f32x16 (
         lane_cols.apply_and_store(g, v, m);
       }
     }
+    wave_lds_fence();  // the next band's writes stay behind this one's reads
   }
 }
 
