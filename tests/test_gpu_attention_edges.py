@@ -58,3 +58,31 @@ def test_nan_keys_reach_every_query_that_sees_them(q_len, q_heads, kv_heads, dim
     c.cache[1][at] = 0xFF  # key scales that read as NaN
     out, lse = c.run()
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("form", ["object", "address", "default object", "default address"])
+def test_the_workspace_belongs_to_the_stream_that_uses_it(form, monkeypatch):
+    """Memory that torch keeps for that stream: freed on return, it is next used by work behind the call."""
+    c = Case([1, 1], [3000, 17], 8, 2, 128, 64, seed=63)
+    assert workspace(c, [1]) > 0
+    r = c.reference()
+    s = torch.cuda.default_stream() if "default" in form else torch.cuda.Stream()
+    owners, empty = [], torch.empty
+
+    def recorded(*args, **kw):
+        owners.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*args, **kw)
+
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        monkeypatch.setattr(torch, "empty", recorded)
+        inputs = [t.to(DEV) for t in (c.q, *c.cache, c.kv_len, c.table)]
+        out, lse = empty((2, 8 * 128), dtype=torch.bfloat16, device=DEV), empty((2, 8), device=DEV)
+        torch.cuda.synchronize()
+        owners.clear()
+        kq.kq_attention_mx(*inputs[:6], out, 8, 2, page_size=64, page_table=inputs[6], lse=lse,
+                           stream=s.cuda_stream if "address" in form else s)
+        monkeypatch.undo()
+        torch.cuda.synchronize()
+    assert owners == [s.cuda_stream] and (s.cuda_stream == 0) == ("default" in form)
+    ref.check_attention(out, lse, r)

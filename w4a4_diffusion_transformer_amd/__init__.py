@@ -346,6 +346,14 @@ def _call(fn, where: str, dev: int, stream, *args):
         raise KQError(status, where)
 
 
+def _stream_object(stream, dev: int):
+    """The torch stream of a `stream` argument.  Address 0 is the default stream; an ExternalStream of it would be
+    another one, of torch's pool."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+
+
 _I32 = (torch.int32,)
 
 
@@ -458,8 +466,7 @@ def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_head
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
         else:  # memory of the stream that uses it, so that its reuse waits for this call
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
-            with torch.cuda.stream(s):
+            with torch.cuda.stream(_stream_object(stream, dev)):
                 workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
     wbytes = 0 if workspace is None else workspace.numel()
     _call(lib().kq_attention_mx, "kq_attention_mx", dev, stream, q, qs, rows,
