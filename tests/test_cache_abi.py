@@ -134,3 +134,14 @@ def test_binding_refuses_what_does_not_fit():
 def test_alloc_cache():
     kc, ks, vc, vs = kq.alloc_cache(5, 96, device="cpu")
     assert kc.shape == vc.shape == (5, 48) and ks.shape == vs.shape == (5, 3) and not kc.any()
+
+
+def test_what_divides_the_keys_of_few_rows(lib):
+    """Key ranges of few rows are balanced over the batch by a sum that fits 32 bits for 512 sequences: no more than
+    that are ever divided."""
+    for batch in (1, 8, 64, 65, 256, 512, 513, 1024, 1025, 65535):
+        for kv_heads, group, dim in ((1, 1, 64), (1, 8, 128), (2, 4, 64), (8, 4, 128), (5, 1, 32), (16, 1, 128)):
+            for cap in (1, 2047, 1 << 14, 1 << 20, 1 << 30):
+                need = lib.kq_attention_mx_workspace(batch, batch, 1, kv_heads * group, kv_heads, dim, cap)
+                assert need == 0 or batch <= 512, (batch, kv_heads, cap)
+    assert lib.kq_attention_mx_workspace(8, 8, 1, 32, 8, 128, 1 << 14) > 0

@@ -86,3 +86,15 @@ def test_the_workspace_belongs_to_the_stream_that_uses_it(form, monkeypatch):
         torch.cuda.synchronize()
     assert owners == [s.cuda_stream] and (s.cuda_stream == 0) == ("default" in form)
     ref.check_attention(out, lse, r)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_more_sequences_than_are_ranked(causal):
+    """65 sequences and more start in their own order, of many rows, the last round divided, and of few."""
+    for n, heads, kv_heads, q, most in ((67, 4, 4, 40, 600), (96, 8, 4, 20, 530), (200, 8, 2, 1, 2300),
+                                        (130, 4, 1, 2, 4100)):
+        kv = [(37 * i * i + 11) % most for i in range(n - 1)] + [most]
+        q_len = [q - (i % 3 if q > 2 else 0) for i in range(n)]
+        c = Case(q_len, kv, heads, kv_heads, 8 if q > 2 else 32, 16, seed=n)
+        assert workspace(c, q_len) > 0, n
+        c.check(causal=causal)

@@ -38,8 +38,6 @@ namespace {
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 
-constexpr int kShareBatch = 1024;  // sequences up to which ranges are balanced over the batch
-
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -640,8 +638,8 @@ constexpr int64_t kTwoHeadKeys = int64_t(1) << 20;  // keys times heads from whi
 // every workgroup of the sequence.
 __device__ __forceinline__ int token_share(const AttnArgs& a, int see, int unit, int lane) {
   int share = (see + a.nsplits - 1) / a.nsplits;
-  if (a.nsplits > 1 && a.batch <= kShareBatch) {
-    auto total = [&](auto&& of) {  // sum over the batch; at most 2^21 tiles a sequence, 2^31 in all
+  if (a.nsplits > 1) {
+    auto total = [&](auto&& of) {  // sum over the batch, 512 sequences at most: with 2^21 tiles each 2^30 in all
       unsigned n = 0;
       for (int i = lane; i < a.batch; i += 64)
         n += of(min((unsigned)(max(0, min(a.kv_len[i], a.capacity)) + 63) >> 6, 1u << 21));
@@ -1127,7 +1125,8 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
     // that fit while it has four; none below eight tiles a wave, where the join and its launch cost as much
     // (1023 keys of one sequence 10.6 us whole, 11.4 in four ranges, called from Python 9.7 and 13.6; of 32
     // sequences 14 whole, 20 in two; 2048 keys of one 17 whole, 11.2 in eight).  Twice as many may be
-    // launched, for the longest sequences of a ragged batch.
+    // launched, for the longest sequences of a ragged batch.  Above 512 workgroups, so above 512 sequences,
+    // nothing is divided.
     const int64_t steps = capacity / unit;
     const int64_t each = steps < 8 ? 1 : std::max(std::min(256 / wgs, steps), std::min(512 / wgs, steps / 4));
     p.nsplits = steps < 8 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({2 * each, steps, 64}));
