@@ -515,9 +515,8 @@ void attn_resident_kernel(AttnArgs a) {
   // XCD i has every head of the row tiles i, i + 8, ...: heads next to each other share cache lines of the
   // codes and, where their rows are not whole lines, of the queries and the outputs
   int id = blockIdx.x;
-  if (a.xcd_units) {
+  if (a.by_xcd) {
     const int unit = id / (8 * a.kv_heads) * 8 + (id & 7);
-    if (unit >= a.xcd_units) return;
     id = unit * a.kv_heads + (id >> 3) % a.kv_heads;
   }
   const RowsWork w = rows_work(a, id);
@@ -1153,7 +1152,7 @@ AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
     p.row_tiles = (int)((groups + p.run_groups - 1) / p.run_groups);
     p.nsplits = 1;
     p.whole = (int)(seqs * p.row_tiles);
-    if (batch * p.row_tiles % 8 == 0) p.xcd_units = (int)(batch * p.row_tiles);
+    p.by_xcd = batch * p.row_tiles % 8 == 0;
   } else {
     const int64_t tiles = batch * kv_heads * p.row_tiles, slots = 256;  // one workgroup a compute unit
     const int64_t rest = tiles % slots;
@@ -1184,11 +1183,10 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   a.whole = p.whole;
   a.split_tiles = p.split_tiles;
   a.run_groups = p.run_groups;
-  a.xcd_units = p.xcd_units;
+  a.by_xcd = p.by_xcd;
   a.row_tiles = p.row_tiles;
   void* kargs[] = {&a};
   int64_t grid = a.whole + (int64_t)a.split_tiles * a.nsplits;
-  if (a.xcd_units) grid = (int64_t)(a.xcd_units + 7) / 8 * 8 * a.kv_heads;
   if (p.few) grid = ((int64_t)a.batch * a.row_tiles * a.nsplits + 7) / 8 * 8 * (a.kv_heads / p.wg_heads);
   const hipError_t e =
       hipLaunchKernel(p.run_groups      ? resident_kernel(a.head_dim)

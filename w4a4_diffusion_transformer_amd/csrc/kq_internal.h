@@ -178,7 +178,8 @@ struct AttnArgs {
   float* part;  // workspace of a split launch
   // set by the launch
   Divisor by_page, by_group;
-  int capacity, group, row_tiles, nsplits, chunks, whole, split_tiles, run_groups, xcd_units;
+  int capacity, group, row_tiles, nsplits, chunks, whole, split_tiles, run_groups;
+  bool by_xcd;
   float c;  // scale * log2(e)
 };
 
@@ -192,7 +193,7 @@ struct AttnPlan {
   int chunks;    // few: key ranges of the whole batch, for each group of heads
   int whole, split_tiles;  // many: tiles that are not divided, and the others
   int run_groups;          // many, with all keys in LDS: 32-row groups of a workgroup (its row tile); else 0
-  int xcd_units;           // of those: row tiles of which one XCD has every head; 0: dealt out singly
+  bool by_xcd;             // of those: every head of a row tile on one XCD (row tiles of the batch: a multiple of 8)
 };
 
 // batch and max_q at least 1.
