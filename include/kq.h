@@ -440,6 +440,10 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
  *
  * head_dim is a multiple of 8 from 8 to 128, q_heads a multiple of kv_heads,
  * scale positive and finite.  lse (fp32 [q_rows][q_heads]) may be NULL.
+ * Limits (KQ_ERR_SHAPE past them): q_rows < 2^28, batch and q_heads <= 65535,
+ * batch * max_q * q_heads and pages_per_seq * page_size <= 2^30, n_slots <
+ * 2^31, and less than 2^32 threads in a launch (65535 sequences of one query:
+ * up to 255 key heads, 510 where a workgroup takes two).
  * Long key ranges with few queries are divided over workgroups and joined in
  * a second launch; the partial results need kq_attention_mx_workspace bytes
  * (0: none, workspace may be NULL), 16-byte aligned, free again when the call

@@ -145,3 +145,14 @@ def test_what_divides_the_keys_of_few_rows(lib):
                 need = lib.kq_attention_mx_workspace(batch, batch, 1, kv_heads * group, kv_heads, dim, cap)
                 assert need == 0 or batch <= 512, (batch, kv_heads, cap)
     assert lib.kq_attention_mx_workspace(8, 8, 1, 32, 8, 128, 1 << 14) > 0
+
+
+def test_attention_past_what_a_launch_holds(lib):
+    """Sizes whose launch would have 2^32 threads or more are refused before it; just below, the checks go on."""
+    a = lambda b, q, group, heads, per, page: attention(lib, q=A, qs=1 << 20, rows=b * q, batch=b, max_q=q, per=per, page=page,
+                                                        n=1 << 20, hq=heads * group, hk=heads, dim=8, os_=1 << 20, lens=None)
+    for ok, sizes in ((True, (65535, 1, 1, 508, 1, 64)), (False, (65535, 1, 1, 512, 1, 64)),    # few rows, two heads
+                      (True, (65535, 1, 1, 252, 0, 64)), (False, (65535, 1, 1, 256, 0, 64)),   # one head
+                      (True, (65535, 1, 36, 60, 1, 64)), (False, (65535, 1, 36, 68, 1, 64)),    # keys on chip
+                      (True, (65535, 1, 36, 124, 1, 1024)), (False, (65535, 1, 36, 132, 1, 1024))):
+        assert a(*sizes) == (NULL if ok else SHAPE), sizes

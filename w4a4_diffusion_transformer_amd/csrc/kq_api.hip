@@ -631,13 +631,15 @@ kq_status kq_attention_mx(const uint16_t* Q, int64_t Q_stride, int64_t q_rows, c
   if (!good_stride(Q_stride, q_width) || !good_stride(out_stride, q_width)) return KQ_ERR_SHAPE;
   if (!(scale > 0.0f) || scale > 3.0e38f) return KQ_ERR_SHAPE;
   if (batch == 0 || max_q == 0) return KQ_OK;
+  const kq::AttnPlan plan = kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity);
+  const kq::AttnLaunch launch = kq::attn_launch(batch, kv_heads, head_dim, plan);
+  if (launch.grid * launch.threads >= int64_t(1) << 32) return KQ_ERR_SHAPE;  // threads of a launch: 32 bits
   if (!Q || !K_codes || !K_scales || !V_codes || !V_scales || !kv_len || !out) return KQ_ERR_NULL;
   if (!aligned(Q, 16) || !aligned(out, 16) || !aligned(K_codes, 16) || !aligned(V_codes, 16) || !aligned(K_scales, 4) ||
       !aligned(V_scales, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(page_table, 4) ||
       !aligned(lse, 4) || !aligned(workspace, 16))
     return KQ_ERR_ALIGN;
-  const int64_t need = kq::attn_workspace(q_rows, q_heads, head_dim,
-                                          kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity));
+  const int64_t need = kq::attn_workspace(q_rows, q_heads, head_dim, plan);
   if (need > 0 && (!workspace || workspace_bytes < need)) return KQ_ERR_WORKSPACE;
   const uint64_t nc = (uint64_t)n_slots * (uint64_t)(kv_heads * head_dim) / 2;
   const Range outs[] = {{out, strided_bytes(q_rows, out_stride, q_width)},

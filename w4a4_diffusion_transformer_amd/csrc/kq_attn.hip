@@ -1168,6 +1168,14 @@ int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, const 
   return p.nsplits * (p.few ? q_rows * q_heads : (int64_t)p.split_tiles * kRowsTile) * (head_dim + 2) * 4;
 }
 
+AttnLaunch attn_launch(int64_t batch, int64_t kv_heads, int64_t head_dim, const AttnPlan& p) {
+  AttnLaunch l{};
+  l.grid = p.few ? (batch * p.row_tiles * p.nsplits + 7) / 8 * 8 * (kv_heads / p.wg_heads)
+                 : p.whole + (int64_t)p.split_tiles * p.nsplits;
+  l.threads = 64 * (p.run_groups ? resident_waves((int)head_dim) : p.wide ? kWideWaves : p.few ? kTokenWaves : kRowsWaves);
+  return l;
+}
+
 hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   AttnArgs a = args;
   a.group = a.q_heads / a.kv_heads;
@@ -1186,17 +1194,14 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t stream) {
   a.by_xcd = p.by_xcd;
   a.row_tiles = p.row_tiles;
   void* kargs[] = {&a};
-  int64_t grid = a.whole + (int64_t)a.split_tiles * a.nsplits;
-  if (p.few) grid = ((int64_t)a.batch * a.row_tiles * a.nsplits + 7) / 8 * 8 * (a.kv_heads / p.wg_heads);
+  const AttnLaunch l = attn_launch(a.batch, a.kv_heads, a.head_dim, p);
   const hipError_t e =
       hipLaunchKernel(p.run_groups      ? resident_kernel(a.head_dim)
                       : !p.few          ? rows_kernel(a.head_dim)
                       : p.wg_heads == 2 ? tokens_kernel<2, kTokenWaves>(a.head_dim)
                       : p.wide          ? tokens_kernel<1, kWideWaves>(a.head_dim)
                                         : tokens_kernel<1, kTokenWaves>(a.head_dim),
-                      dim3((unsigned)grid),
-                      dim3(64 * (p.run_groups ? resident_waves(a.head_dim) : p.wide ? kWideWaves : p.few ? kTokenWaves : kRowsWaves)), kargs, 0,
-                      stream);
+                      dim3((unsigned)l.grid), dim3(l.threads), kargs, 0, stream);
   if (e != hipSuccess || a.nsplits == 1) return e;
   int slices = 1;
   // two ranges a lane (few rows) or four, all in flight: 16384 keys of one sequence 17.0 us, 18.0 one by one

@@ -199,6 +199,12 @@ struct AttnPlan {
 // batch and max_q at least 1.
 AttnPlan attn_plan(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                    int64_t capacity);
+// The first launch of a call so divided.
+struct AttnLaunch {
+  int64_t grid;
+  int threads;
+};
+AttnLaunch attn_launch(int64_t batch, int64_t kv_heads, int64_t head_dim, const AttnPlan& plan);
 int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, const AttnPlan& plan);
 hipError_t launch_attn(const AttnArgs& args, hipStream_t stream);
 
