@@ -98,3 +98,29 @@ def test_more_sequences_than_are_ranked(causal):
         c = Case(q_len, kv, heads, kv_heads, 8 if q > 2 else 32, 16, seed=n)
         assert workspace(c, q_len) > 0, n
         c.check(causal=causal)
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_the_default_share_of_a_cache(q_len):
+    """Without a table or a page size each sequence has an equal share: of more slots than a page may have (2^24), and
+    of fewer slots than there are sequences, where every query is empty."""
+    for n, batch in (((1 << 24) + 70, 1), (2 * (1 << 24) + 131, 2), (2, 3)):
+        cache = [torch.zeros((n, w), dtype=torch.uint8, device=DEV) for w in (16, 1, 16, 1)]
+        share = n // batch
+        kv_len = torch.tensor([min(share, 333 + i) for i in range(batch)], dtype=torch.int32)
+        for i in range(batch if share else 0):
+            at = torch.arange(kv_len[i]) + i * share
+            for j, s in ((0, 1), (2, 2)):
+                codes, scales = ref.quantize(ref.bf16((len(at), 32), 10 * i + s))
+                cache[j][at.to(DEV)], cache[j + 1][at.to(DEV)] = codes.to(DEV), scales.to(DEV)
+        q = ref.bf16((batch * q_len, 64), 3)
+        out = torch.full((batch * q_len, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((batch * q_len, 2), 7.0, device=DEV)
+        kq.kq_attention_mx(q.to(DEV), *cache, kv_len.to(DEV), out, 2, 1, lse=lse)
+        if share == 0:
+            assert not out.any() and torch.isneginf(lse).all()
+            continue
+        small = torch.cat([torch.arange(333 + batch) + i * share for i in range(batch)]).to(DEV)  # the slots that have keys
+        table = torch.arange(batch, dtype=torch.int32)[:, None]
+        ref.check_attention(out, lse, ref.attention(q, [t[small].cpu() for t in cache], kv_len, table, 333 + batch, 2, 1,
+                                                    [i * q_len for i in range(batch + 1)]))

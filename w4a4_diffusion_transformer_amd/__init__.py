@@ -355,6 +355,7 @@ def _stream_object(stream, dev: int):
 
 
 _I32 = (torch.int32,)
+_PAGE = 1 << 24  # slots of a page at most
 
 
 def kq_gemm_mx_ex(a_codes, a_scales, b_codes, b_scales, bias=None, act: int = KQ_ACT_NONE, gate=None,
@@ -453,8 +454,9 @@ def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_head
         pages_per_seq = page_table.shape[1]
         if page_size is None:
             raise ValueError("page_size is needed with a page_table")
-    elif page_size is None:
-        page_size, pages_per_seq = max(1, n // max(1, batch)), 1
+    elif page_size is None:  # one page each, or, of more slots than a page may have, a page a slot; no slots: no pages
+        share = n // max(1, batch)
+        page_size, pages_per_seq = (share, 1) if 0 < share <= _PAGE else (1, share)
     elif pages_per_seq is None:
         pages_per_seq = n // page_size // max(1, batch)
     if max_q is None:
