@@ -439,7 +439,8 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
  * that do not see its key.
  *
  * head_dim is a multiple of 8 from 8 to 128, q_heads a multiple of kv_heads,
- * scale positive and finite.  lse (fp32 [q_rows][q_heads]) may be NULL.
+ * scale positive and at most 2^127 (scale q.k itself has to stay within fp32,
+ * as every score does).  lse (fp32 [q_rows][q_heads]) may be NULL.
  * Limits (KQ_ERR_SHAPE past them): q_rows < 2^28, batch and q_heads <= 65535,
  * batch * max_q * q_heads and pages_per_seq * page_size <= 2^30, n_slots <
  * 2^31, and less than 2^32 threads in a launch (65535 sequences of one query:

@@ -156,3 +156,11 @@ def test_attention_past_what_a_launch_holds(lib):
                       (True, (65535, 1, 36, 60, 1, 64)), (False, (65535, 1, 36, 68, 1, 64)),    # keys on chip
                       (True, (65535, 1, 36, 124, 1, 1024)), (False, (65535, 1, 36, 132, 1, 1024))):
         assert a(*sizes) == (NULL if ok else SHAPE), sizes
+
+
+def test_attention_scale_and_its_multiple_are_finite(lib):
+    """The kernels work in powers of two: scale * log2(e) has to be finite too."""
+    for scale in (2.0 ** 127 * 1.001, 2.9e38, 3.2e38, float("inf")):
+        assert attention(lib, scale=scale, lens=None) == SHAPE, scale
+    for scale in (2.0 ** 127, 1e-30, 1.0):
+        assert attention(lib, scale=scale, lens=None) == NULL, scale

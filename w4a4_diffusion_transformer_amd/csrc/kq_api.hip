@@ -629,7 +629,7 @@ kq_status kq_attention_mx(const uint16_t* Q, int64_t Q_stride, int64_t q_rows, c
   if (!q_start && batch * max_q > q_rows) return KQ_ERR_SHAPE;
   const int64_t q_width = q_heads * head_dim;
   if (!good_stride(Q_stride, q_width) || !good_stride(out_stride, q_width)) return KQ_ERR_SHAPE;
-  if (!(scale > 0.0f) || scale > 3.0e38f) return KQ_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 0x1p127f) return KQ_ERR_SHAPE;  // times log2(e) finite
   if (batch == 0 || max_q == 0) return KQ_OK;
   const kq::AttnPlan plan = kq::attn_plan(batch, max_q, q_heads, kv_heads, head_dim, capacity);
   const kq::AttnLaunch launch = kq::attn_launch(batch, kv_heads, head_dim, plan);
