@@ -445,8 +445,9 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
  * batch * max_q * q_heads and pages_per_seq * page_size <= 2^30, n_slots <
  * 2^31, and less than 2^32 threads in a launch (65535 sequences of one query:
  * up to 255 key heads, 510 where a workgroup takes two).
- * Long key ranges with few queries are divided over workgroups and joined in
- * a second launch; the partial results need kq_attention_mx_workspace bytes
+ * Long key ranges with few queries, and of many queries those that the GPU
+ * would compute last and not all at work, are divided over workgroups and
+ * joined in a second launch; the partial results need kq_attention_mx_workspace bytes
  * (0: none, workspace may be NULL), 16-byte aligned, free again when the call
  * has run: calls that may run at the same time, two captured graphs among
  * them, need one each.  The division depends on the sizes and the lengths

@@ -440,8 +440,9 @@ def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_head
     [q_rows, q_heads], or None).
 
     kv_len int32 [batch]; page_table int32 [batch, pages_per_seq], or None: the sequences' slots in order, of
-    pages_per_seq * page_size each (by default an equal share of the cache).  q_start int32 [batch + 1] (max_q bounds
-    its differences, by default all rows), or None: max_q rows each (by default an equal share).  scale defaults to
+    pages_per_seq * page_size each (by default an equal share of the cache).  q_start int32 [batch + 1], or None: max_q
+    rows each (by default an equal share).  With q_start, max_q bounds its differences: pass it, for the call is divided
+    by it (all rows, the default, is right and slow: each sequence then has room for every row).  scale defaults to
     head_dim ** -0.5.  workspace (uint8, kq_attention_mx_workspace bytes) is allocated for the call if None."""
     rows, width = Q.shape
     batch = kv_len.shape[0]

@@ -104,8 +104,11 @@ __device__ __forceinline__ void lds_barrier() {
 // accumulators spilled 52 registers, and the 8192 x 4608 x 1152 product with
 // bias and GELU took 90 us.)  Residual rows are loaded a band ahead, and the
 // gate is kept in registers where the wave's rows are of one sample: with
-// bias, gate and residual that product went from 98 to 73 us (the product
-// alone: 48).  Non-temporal stores: 2-7% faster than device scope or the default here.
+// bias, gate and residual that product went from 98 to 73 us.  Non-temporal
+// stores: 2-7% faster than device scope or the default here.  (20 calls in a
+// captured graph, in us: without any part 46, with a bias 48, and GELU 54,
+// with bias, gate and residual 67; kq_gemm_mx 45 with four outputs in turn, 39
+// with one, which then stays in the last-level cache.)
 constexpr int kBandStride = 68;               // floats per row of a band: 64 and a pad against bank conflicts
 constexpr int kBandF = 32 * kBandStride;      // floats per wave
 
@@ -505,8 +508,9 @@ hipError_t launch_gemm(const GemmArgs& args, hipStream_t stream) {
   const int64_t gn = (g.N + kBN - 1) / kBN;
   // With an epilogue, a product whose 256-row tiles fill between a half and all
   // of the GPU takes 192-row tiles where those still run in one round (4096 x
-  // 2240 x 5600: 198 tiles, 49 us, against 144 in 54 us; at half or less the
-  // tiles are halved below: 1024 x 4608 x 1152 14 us against 18).
+  // 2240 x 5600 with bias, gate and residual: 198 tiles, 49 us, against 144 in
+  // 57 us; at half or less the tiles are halved below: 1024 x 4608 x 1152 14 us
+  // against 18).
   const int64_t whole = gn * ((g.M + kBM - 1) / kBM);
   g.tile_mi = g.epi.on && whole < slots && 2 * whole > slots && gn * ((g.M + 191) / 192) <= slots ? 3 : 4;
   const int bm = 64 * g.tile_mi;
