@@ -350,10 +350,12 @@ kq_status run_cache(bool write, const uint16_t* k, int64_t k_stride, const uint1
 }
 
 // Whether kq_gemm_mx_ex takes the few-row form: its time goes with the outputs, as the tile form's does not while its
-// tiles fit the GPU at once, and with K as the tile form's.  Measured around the limit, few-row against tiles (us):
-// 256 x 4608 x 1152 9.7 and 12.1, 256 x 6912 x 1152 14.0 and 12.5, 128 x 9216 x 2240 16.2 and 18.9, 256 x 9216 x 2240
-// 25.5 and 19.6, 1024 x 1152 x 4608 24.1 and 26.0, 1024 x 2240 x 5600 45.9 and 38.1, 256 x 4608 x 12288 52 and 58.
-// Neither is near what 64 to 1024 rows over a long K could take (the last two: 7 and 8 us of operations).
+// tiles fit the GPU at once, and with K as the tile form's.  Measured around the limit, few-row against tiles (us, with
+// a bias), at K = 320, 1152, 4608 and 12288: below it 256 x 4608 8.5 and 8.5, 10.2 and 10.5, 24.0 and 24.1, 51.7 and
+// 56.5, and 1024 x 1152 8.5 and 8.4, 10.3 and 10.4, 23.6 and 24.3, 59.4 and 58.6 (worst: 128 x 9216 x 12288 61.2 and
+// 53.2); above it 256 x 6912 11.1 and 8.6, 13.6 and 10.8, 31.6 and 24.3, 68.1 and 56.5, and 1024 x 1408 9.4 and 8.5,
+// 11.8 and 10.6, 25.9 and 24.3, 64.3 and 57.0.  Neither is near what 64 to 1024 rows over a long K could take
+// (256 x 4608 x 12288: 7.5 us of operations).
 bool few_rows(int64_t M, int64_t N) { return M * N <= (int64_t(5) << 18); }
 
 // Shared body of kq_gemm_mx (no epilogue) and kq_gemm_mx_ex.

@@ -515,7 +515,9 @@ void attn_resident_kernel(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   // XCD i has every head of the row tiles i, i + 8, ...: heads next to each other share cache lines of the
-  // codes and, where their rows are not whole lines, of the queries and the outputs
+  // codes and, where their rows are not whole lines, of the queries and the outputs (8 x 4096 rows of 16 heads
+  // over up to 300 keys: of 72 channels 76.1 us, dealt out singly 78.7; of 64 70.9 and 72.7; 24 heads of 128 level;
+  // 4 x 4096 rows of 96 51.8 and 50.4)
   int id = blockIdx.x;
   if (a.by_xcd) {
     const int unit = id / (8 * a.kv_heads) * 8 + (id & 7);
