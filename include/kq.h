@@ -126,7 +126,7 @@ typedef enum {
 typedef enum { KQ_FRONT_KRON = 0, KQ_FRONT_PLAIN = 1, KQ_FRONT_SMOOTH = 2, KQ_FRONT_HADAMARD = 3 } kq_front;
 
 /* ABI version of this header (bumped on any signature or layout change). */
-#define KQ_ABI_VERSION 7
+#define KQ_ABI_VERSION 8
 int kq_abi_version(void);
 
 /* Static, never-NULL description of a status code. */
@@ -462,6 +462,105 @@ kq_status kq_attention_mx(const uint16_t* Q, int64_t Q_stride, int64_t q_rows, c
                           int64_t page_size, const int32_t* kv_len, int64_t q_heads, int64_t kv_heads,
                           int64_t head_dim, float scale, int causal, uint16_t* out, int64_t out_stride, float* lse,
                           void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Norms over channels: none, x / sqrt(mean x^2 + eps), (x - mean) / sqrt(mean (x - mean)^2 + eps). */
+typedef enum { KQ_NORM_NONE = 0, KQ_NORM_RMS = 1, KQ_NORM_LAYER = 2 } kq_norm;
+
+/* Which channels of a head are pair p of the R/2 that turn: 2p and 2p + 1, or p and p + R/2. */
+typedef enum { KQ_ROPE_PAIRS = 0, KQ_ROPE_HALVES = 1 } kq_rope_layout;
+
+/*
+ * Rotary positions with several axes (a token's place in a text; its time, row
+ * and column in a video).  axis_dims[i] channels of each head (even, positive)
+ * turn with axis i, the pairs of axis 0 first; R is their sum, at most
+ * head_dim, and channels from R on do not turn.  Pair p of axis i turns by
+ * positions[t][i] * freqs[p] radians.  This struct lies in host memory and is
+ * read before the call returns; positions and freqs are device memory.  A NULL
+ * rotation, or n_axes 0, turns nothing.
+ */
+typedef struct {
+  const int32_t* positions; /* [tokens][n_axes] */
+  const double* freqs;      /* [R/2], finite; an angle below 2^48 in size */
+  int32_t n_axes;           /* 0 .. 4 */
+  int32_t axis_dims[4];
+  kq_rope_layout layout;
+} kq_rotation;
+
+/*
+ * Rows of heads (queries, keys) normalised and turned: for each head of
+ * head_dim channels (a multiple of 8, 8 .. 128) of row t
+ *   n = x                                        norm KQ_NORM_NONE, or
+ *   n = x weight / sqrt(mean(x^2) + eps)         KQ_NORM_RMS (weight fp32 [head_dim], NULL: 1);
+ *   (u, v) of a pair -> (u cos a - v sin a, u sin a + v cos a),
+ * rounded once to bf16: everything before is fp64, the angles too, so far
+ * positions keep theirs (to 2^-52 of the angle, and 2^-40).  X and out are
+ * bf16 [tokens][heads * head_dim] at strides X_stride and out_stride
+ * (elements, a multiple of 8), 16-byte aligned; out may be X itself at the
+ * same stride, or other columns of the same matrix; any other overlap is
+ * KQ_ERR_ALIAS.  KQ_NORM_LAYER and unknown layouts are KQ_ERR_VARIANT; axes
+ * that are odd, negative or more than head_dim together KQ_ERR_SHAPE.
+ * weight and positions 4-byte, freqs 8-byte aligned.
+ */
+kq_status kq_rope(const uint16_t* X, int64_t X_stride, int64_t tokens, int64_t heads, int64_t head_dim, kq_norm norm,
+                  const float* weight, float eps, const kq_rotation* rotation, uint16_t* out, int64_t out_stride,
+                  hipStream_t stream);
+
+/*
+ * kq_cache_write of keys that are normalised and turned on the way, with the
+ * queries of the same tokens turned in the same launch: K's heads as kq_rope
+ * (with k_weight) and then, from that bf16, as kq_cache_write; V as
+ * kq_cache_write (V may be NULL); Q, unless NULL, as kq_rope with q_weight
+ * into Q_out.  The results equal those calls', bit for bit.  A token without a
+ * slot still has its query turned.  kv_heads * head_dim is a multiple of 32;
+ * q_heads is any positive number, read only with Q.  Q_out may be Q itself and
+ * Q, K and V columns of one matrix: a fused projection's output can be
+ * passed as it is and its queries turned in place.  Otherwise as kq_rope and
+ * kq_cache_write.
+ */
+kq_status kq_cache_write_rope(const uint16_t* Q, int64_t Q_stride, int64_t q_heads, const float* q_weight,
+                              uint16_t* Q_out, int64_t Q_out_stride, const uint16_t* K, int64_t K_stride,
+                              const uint16_t* V, int64_t V_stride, int64_t tokens, int64_t kv_heads, int64_t head_dim,
+                              kq_norm norm, const float* k_weight, float eps, const kq_rotation* rotation,
+                              const int32_t* slots, int64_t n_slots, uint8_t* K_codes, uint8_t* K_scales,
+                              uint8_t* V_codes, uint8_t* V_scales, hipStream_t stream);
+
+/*
+ * The residual stream between two blocks: what a block gave (Y) is normalised
+ * and gated and added to the stream X, and the next block's input is taken
+ * from the sum.  Per row t of sample s = t / tokens_per_sample:
+ *   u  = N_post(y) * post_weight * gate[s]             post_weight fp32 [d], gate fp32 [samples][d], each may be NULL
+ *   x' = residual_scale * x + u                        -> X_out, bf16
+ *   h  = N_pre(x') * pre_weight * (1 + mod_scale[s]) + mod_shift[s]
+ *                                                      -> H, bf16, and / or out_codes and out_scales, as
+ *                                                         kq_mx_quantize of that bf16 matrix, and / or
+ *   row_stats[t] = (mean, 1 / sqrt(var + eps)) of x'   fp32, as kq_row_stats (mean 0 for KQ_NORM_RMS): what
+ *                                                      kq_quantize_adaln reads to transform and quantize x'
+ * with the norms of kq_norm over the row's d channels, statistics of x' taken
+ * from the bf16 values that are stored, and samples = ceil(tokens /
+ * tokens_per_sample).  Arithmetic and sums are fp64 up to each rounding.  h is
+ * rounded once, so it may differ by a bf16 step from what kq_quantize_adaln
+ * forms in fp32 steps.
+ *
+ * Y NULL: the stream is X as it is (x' = x, the first block's norm): X_out,
+ * post, post_weight, gate have to be NULL / KQ_NORM_NONE and residual_scale 1
+ * (KQ_ERR_VARIANT otherwise).  With Y, X_out is needed and H, codes and
+ * statistics may all be NULL.  out_codes and out_scales come together.
+ * row_stats needs a norm (KQ_ERR_VARIANT).  tokens_per_sample is any positive
+ * number, read with gate, mod_scale or mod_shift.
+ *
+ * X, Y, X_out and H are rows at strides in elements (a multiple of 8, at least
+ * d; d a multiple of 32), 16-byte aligned, vectors 16-byte, row_stats 8-byte
+ * aligned.  X_out may be X itself at the same stride (the stream updated in
+ * place); rows may be columns of one matrix that do not touch; any other
+ * overlap is KQ_ERR_ALIAS.  eps >= 0 and residual_scale finite
+ * (KQ_ERR_SHAPE).
+ */
+kq_status kq_residual_norm(const uint16_t* X, int64_t X_stride, const uint16_t* Y, int64_t Y_stride, int64_t tokens,
+                           int64_t d, kq_norm post, const float* post_weight, const float* gate, float residual_scale,
+                           uint16_t* X_out, int64_t X_out_stride, kq_norm pre, const float* pre_weight,
+                           const float* mod_scale, const float* mod_shift, int64_t tokens_per_sample, float eps,
+                           uint16_t* H, int64_t H_stride, uint8_t* out_codes, uint8_t* out_scales, float* row_stats,
+                           hipStream_t stream);
 
 /*
  * Measurement entry (not a quantizer): moves exactly the traffic of

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,6 +25,8 @@ __all__ = [
     "kq_build_blocks_inverse_t", "kq_gemm_mx", "kq_hadamard_quantize_ex", "kq_build_blocks16", "kq_tune",
     "kq_tune_reset", "kq_stream_probe", "KQ_ACT_NONE", "KQ_ACT_GELU_TANH", "KQ_ACT_GELU_ERF", "KQ_ACT_SILU",
     "kq_gemm_mx_ex", "alloc_cache", "kq_cache_write", "kq_cache_read", "kq_attention_mx", "kq_attention_mx_workspace",
+    "KQ_NORM_NONE", "KQ_NORM_RMS", "KQ_NORM_LAYER", "KQ_ROPE_PAIRS", "KQ_ROPE_HALVES", "Rotation", "rope_freqs", "kq_rope",
+    "kq_cache_write_rope", "kq_residual_norm",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkq.so")
@@ -31,6 +34,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkq.so")
 KQ_AUTO, KQ_MFMA_DENSE, KQ_MFMA_OTF, KQ_BUTTERFLY = 0, 1, 2, 3
 KQ_FRONT_KRON, KQ_FRONT_PLAIN, KQ_FRONT_SMOOTH, KQ_FRONT_HADAMARD = 0, 1, 2, 3
 KQ_ACT_NONE, KQ_ACT_GELU_TANH, KQ_ACT_GELU_ERF, KQ_ACT_SILU = 0, 1, 2, 3
+KQ_NORM_NONE, KQ_NORM_RMS, KQ_NORM_LAYER = 0, 1, 2
+KQ_ROPE_PAIRS, KQ_ROPE_HALVES = 0, 1
 VARIANTS = {"auto": KQ_AUTO, "mfma_dense": KQ_MFMA_DENSE, "mfma_otf": KQ_MFMA_OTF, "butterfly": KQ_BUTTERFLY}
 
 _lib = None
@@ -81,7 +86,13 @@ def lib() -> ctypes.CDLL:
                                       cf, ci, vp, i64, vp, vp, i64, vp]
         L.kq_attention_mx_workspace.argtypes = [i64] * 7
         L.kq_attention_mx_workspace.restype = i64
-        for name in ("kq_gemm_mx_ex", "kq_cache_write", "kq_cache_read", "kq_attention_mx"):
+        L.kq_rope.argtypes = [vp, i64, i64, i64, i64, ci, vp, cf, vp, vp, i64, vp]
+        L.kq_cache_write_rope.argtypes = [vp, i64, i64, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, ci, vp, cf, vp, vp,
+                                          i64, vp, vp, vp, vp, vp]
+        L.kq_residual_norm.argtypes = [vp, i64, vp, i64, i64, i64, ci, vp, vp, cf, vp, i64, ci, vp, vp, vp, i64, cf, vp,
+                                       i64, vp, vp, vp, vp]
+        for name in ("kq_gemm_mx_ex", "kq_cache_write", "kq_cache_read", "kq_attention_mx", "kq_rope",
+                     "kq_cache_write_rope", "kq_residual_norm"):
             getattr(L, name).restype = ci
         for name in ("kq_build_blocks", "kq_quantize", "kq_quantize_ex", "kq_mx_quantize", "kq_stream_probe",
                      "kq_smooth_quantize",
@@ -479,3 +490,116 @@ def kq_attention_mx(Q, k_codes, k_scales, v_codes, v_scales, kv_len, out, q_head
           causal, o, os_, _full(lse, "lse", _F32, (rows, q_heads), dev),
           _full(workspace, "workspace", _U8, (wbytes,), dev), wbytes)
     return out, lse
+
+
+class _CRotation(ctypes.Structure):
+    """kq_rotation of the C ABI."""
+    _fields_ = [("positions", ctypes.c_void_p), ("freqs", ctypes.c_void_p), ("n_axes", ctypes.c_int32),
+                ("axis_dims", ctypes.c_int32 * 4), ("layout", ctypes.c_int)]
+
+
+class Rotation(NamedTuple):
+    """Rotary positions: the places of tokens (int32 [tokens, axes]), radians a position of each pair of channels
+    (float64 [sum(axis_dims) / 2], axis by axis; rope_freqs), channels that turn with each axis, and whether a pair is
+    channels p and p + sum(axis_dims) / 2 of a head (halves) or 2 p and 2 p + 1."""
+    positions: torch.Tensor
+    freqs: torch.Tensor
+    axis_dims: tuple
+    halves: bool = False
+
+
+def rope_freqs(axis_dims, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """base ** (-2 i / dim) for each pair i of each axis of dim channels, in axis order (float64)."""
+    return torch.cat([float(base) ** (-torch.arange(0, a, 2, dtype=torch.float64) / a) for a in axis_dims]).to(device)
+
+
+def _rotation(rotation, tokens: int, dev: int):
+    """The C struct of a Rotation (None stays None), its tensors checked."""
+    if rotation is None:
+        return None
+    dims = rotation.axis_dims
+    n = len(dims)
+    if n > 4:
+        raise ValueError(f"axis_dims: at most 4 axes, got {n}")
+    if any(not 0 < a <= 128 or a % 2 for a in dims):
+        raise ValueError(f"axis_dims: even numbers from 2 to 128, got {tuple(dims)}")
+    return _CRotation(_full(rotation.positions, "positions", _I32, (tokens, n), dev),
+                      _full(rotation.freqs, "freqs", (torch.float64,), (sum(dims) // 2,), dev), n,
+                      (ctypes.c_int32 * 4)(*dims), KQ_ROPE_HALVES if rotation.halves else KQ_ROPE_PAIRS)
+
+
+def _head_dim(width: int, heads: int, what: str) -> int:
+    if heads < 1 or width % heads:
+        raise ValueError(f"{what}: {width} columns are not {heads} heads")
+    return width // heads
+
+
+def kq_rope(X, out, heads: int, rotation: Rotation | None = None, norm: int = KQ_NORM_NONE, weight=None,
+            eps: float = 1e-6, stream=None):
+    """The heads of X (bfloat16 [tokens, heads * head_dim]) normalised (KQ_NORM_RMS, weight float32 [head_dim] or None)
+    and turned by their positions into out, which may be X."""
+    tokens, width = X.shape
+    dim = _head_dim(width, heads, "X")
+    dev = _device(X, "X")
+    x, xs = _rows(X, "X", width, tokens, dev)
+    o, os_ = _rows(out, "out", width, tokens, dev)
+    turn = _rotation(rotation, tokens, dev)
+    _call(lib().kq_rope, "kq_rope", dev, stream, x, xs, tokens, heads, dim, norm,
+          _full(weight, "weight", _F32, (dim,), dev), eps, None if turn is None else ctypes.addressof(turn), o, os_)
+    return out
+
+
+def kq_cache_write_rope(K, V, slots, k_codes, k_scales, v_codes, v_scales, kv_heads: int,
+                        rotation: Rotation | None = None, norm: int = KQ_NORM_NONE, k_weight=None, eps: float = 1e-6,
+                        Q=None, q_out=None, q_heads: int = 0, q_weight=None, stream=None):
+    """kq_cache_write with the heads of K normalised and turned as kq_rope does, and, with Q, kq_rope of Q's heads into
+    q_out (which may be Q) in the same launch.  V and Q may be None; Q, K and V may be columns of one matrix."""
+    dev = _device(K, "K")
+    tokens, W, k, ks, v, vs, at = _cache_rows(K, V, slots, dev)
+    dim = _head_dim(W, kv_heads, "K")
+    n, pools = _cache(k_codes, k_scales, v_codes, v_scales, W, dev, V is not None)
+    q, qs, o, os_ = None, 8, None, 8
+    if Q is not None:
+        if q_heads < 1:
+            raise ValueError("q_heads is needed with Q")
+        q, qs = _rows(Q, "Q", q_heads * dim, tokens, dev)
+        o, os_ = _rows(q_out, "q_out", q_heads * dim, tokens, dev)
+    turn = _rotation(rotation, tokens, dev)
+    _call(lib().kq_cache_write_rope, "kq_cache_write_rope", dev, stream, q, qs, q_heads,
+          _full(q_weight, "q_weight", _F32, (dim,), dev), o, os_, k, ks, v, vs, tokens, kv_heads, dim, norm,
+          _full(k_weight, "k_weight", _F32, (dim,), dev), eps, None if turn is None else ctypes.addressof(turn), at, n,
+          *pools)
+    return k_codes, k_scales, v_codes, v_scales
+
+
+def kq_residual_norm(X, Y, x_out, post: int = KQ_NORM_NONE, post_weight=None, gate=None, residual_scale: float = 1.0,
+                     pre: int = KQ_NORM_NONE, pre_weight=None, mod_scale=None, mod_shift=None,
+                     tokens_per_sample: int | None = None, eps: float = 1e-6, h=None, out_codes=None, out_scales=None,
+                     row_stats=None, stream=None):
+    """x_out = residual_scale * X + gate * norm(Y) * post_weight, and of it the next block's input
+    norm(x_out) * pre_weight * (1 + mod_scale) + mod_shift into h (bfloat16) and / or as MXFP4 into out_codes and
+    out_scales, and / or its row statistics (float32 [tokens, 2]) for kq_quantize_adaln.
+
+    Rows are bfloat16 [tokens, d]; x_out may be X.  Y and x_out None: the stream is X as it is.  Weights float32 [d],
+    gate, mod_scale and mod_shift float32 [samples, d] of tokens_per_sample rows each (default: one sample)."""
+    tokens, d = X.shape
+    dev = _device(X, "X")
+    per = tokens if tokens_per_sample is None else int(tokens_per_sample)
+    sampled = gate is not None or mod_scale is not None or mod_shift is not None
+    if sampled and per <= 0 < tokens:
+        raise ValueError("tokens_per_sample must be positive")
+
+    def rows(t, what):
+        return (None, d) if t is None else _rows(t, what, d, tokens, dev)
+
+    def vectors(t, what):
+        return None if t is None else _full(t, what, _F32, (-(-tokens // per) if tokens else t.shape[0], d), dev)
+
+    _call(lib().kq_residual_norm, "kq_residual_norm", dev, stream, *rows(X, "X"), *rows(Y, "Y"), tokens, d, post,
+          _full(post_weight, "post_weight", _F32, (d,), dev), vectors(gate, "gate"), residual_scale,
+          *rows(x_out, "x_out"), pre, _full(pre_weight, "pre_weight", _F32, (d,), dev), vectors(mod_scale, "mod_scale"),
+          vectors(mod_shift, "mod_shift"), per or 1, eps, *rows(h, "h"),
+          _full(out_codes, "out_codes", _U8, (tokens, d // 2), dev),
+          _full(out_scales, "out_scales", _U8, (tokens, d // 32), dev),
+          _full(row_stats, "row_stats", _F32, (tokens, 2), dev))
+    return x_out, h

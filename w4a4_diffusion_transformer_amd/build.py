@@ -27,7 +27,7 @@ FLAGS = [
 ]
 
 SOURCES = ["kq_api.hip", "kq_mfma.hip", "kq_quad.hip", "kq_flat.hip", "kq_build.hip", "kq_stats.hip", "kq_gemm.hip",
-           "kq_gemm_rows.hip", "kq_cache.hip", "kq_attn.hip"]
+           "kq_gemm_rows.hip", "kq_cache.hip", "kq_attn.hip", "kq_rope.hip", "kq_norm.hip"]
 
 
 def _compile(src: str) -> str:

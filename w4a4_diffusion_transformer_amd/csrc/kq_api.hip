@@ -297,12 +297,25 @@ bool good_stride(int64_t stride, int64_t width) {
   return stride >= width && stride % 8 == 0 && stride <= (int64_t(1) << 31);
 }
 
-// Whether two row sets of the same count and width, at the same stride, interleave without touching (column
-// ranges of one matrix).
-bool columns_apart(const uint16_t* x, const uint16_t* y, int64_t stride, int64_t width) {
+// Whether two row sets of the same count, of these widths and at the same stride, interleave without touching
+// (column ranges of one matrix).
+bool columns_apart(const uint16_t* x, int64_t x_width, const uint16_t* y, int64_t y_width, int64_t stride) {
   int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) / 2 % stride;  // y may lie below
   if (d < 0) d += stride;
-  return d >= width && d + width <= stride;
+  return d >= x_width && d + y_width <= stride;
+}
+
+// Rows of bf16 at a stride, as an argument (p NULL: not there).
+struct Rows {
+  const uint16_t* p;
+  int64_t stride, width;
+  Range range(int64_t tokens) const { return {p, p ? strided_bytes(tokens, stride, width) : 0}; }
+};
+
+// Whether rows that are written touch others, which column ranges of one matrix do not.
+bool rows_touch(const Rows& a, const Rows& b, int64_t tokens) {
+  return overlap(a.range(tokens), b.range(tokens)) &&
+         !(a.stride == b.stride && columns_apart(a.p, a.width, b.p, b.width, a.stride));
 }
 
 // Shared body of kq_cache_write and kq_cache_read.  k / v: the rows, read (write) or written (read).
@@ -327,7 +340,7 @@ kq_status run_cache(bool write, const uint16_t* k, int64_t k_stride, const uint1
     for (const Range& r : rows)
       if (any_alias(&r, 1, pools, 4) || any_alias(&r, 1, table, 1)) return KQ_ERR_ALIAS;
     // the two outputs may be column ranges of one matrix
-    if (overlap(rows[0], rows[1]) && !(k_stride == v_stride && columns_apart(k, v, k_stride, width)))
+    if (overlap(rows[0], rows[1]) && !(k_stride == v_stride && columns_apart(k, width, v, width, k_stride)))
       return KQ_ERR_ALIAS;
   }
   if (write && n_slots == 0) return KQ_OK;
@@ -347,6 +360,81 @@ kq_status run_cache(bool write, const uint16_t* k, int64_t k_stride, const uint1
   a.v_codes = const_cast<uint8_t*>(vc);
   a.v_scales = const_cast<uint8_t*>(vs);
   return from_hip(kq::launch_cache(write, v != nullptr, a, stream));
+}
+
+// Shared body of kq_rope (queries alone) and kq_cache_write_rope (V and Q may be missing).
+kq_status run_rope(const Rows& q, int64_t q_heads, const float* q_weight, const Rows& q_out, const Rows& k, const Rows& v,
+                   int64_t tokens, int64_t kv_heads, int64_t head_dim, kq_norm norm, const float* k_weight, float eps,
+                   const kq_rotation* rotation, const int32_t* slots, int64_t n_slots, uint8_t* kc, uint8_t* ks,
+                   uint8_t* vc, uint8_t* vs, hipStream_t stream) {
+  const bool cache = kv_heads > 0;
+  if (head_dim <= 0 || head_dim > 128 || head_dim % 8 != 0) return KQ_ERR_SHAPE;
+  for (int64_t heads : {q_heads, kv_heads}) {
+    if (heads > (int64_t(1) << 21)) return KQ_ERR_SHAPE;
+    if (heads == 0) continue;
+    // check_shape for whole blocks of 32; rows that are not quantized need not be
+    const kq_status st = check_shape(tokens, (heads * head_dim + 31) / 32 * 32);
+    if (st != KQ_OK) return st;
+  }
+  if (cache && kv_heads * head_dim % 32 != 0) return KQ_ERR_SHAPE;
+  if (n_slots < 0 || n_slots >= (int64_t(1) << 31)) return KQ_ERR_SHAPE;
+  for (const Rows* r : {&q, &q_out, &k, &v})
+    if (r->p && !good_stride(r->stride, r->width)) return KQ_ERR_SHAPE;
+  if (norm != KQ_NORM_NONE && norm != KQ_NORM_RMS) return KQ_ERR_VARIANT;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return KQ_ERR_SHAPE;
+  const int axes = rotation ? rotation->n_axes : 0;
+  int64_t turned = 0;
+  if (axes < 0 || axes > 4) return KQ_ERR_SHAPE;
+  for (int i = 0; i < axes; ++i) {
+    if (rotation->axis_dims[i] <= 0 || rotation->axis_dims[i] % 2 != 0) return KQ_ERR_SHAPE;
+    turned += rotation->axis_dims[i];
+  }
+  if (turned > head_dim) return KQ_ERR_SHAPE;
+  if (axes > 0 && rotation->layout != KQ_ROPE_PAIRS && rotation->layout != KQ_ROPE_HALVES) return KQ_ERR_VARIANT;
+  if (tokens == 0) return KQ_OK;
+  if ((q_heads > 0 && (!q.p || !q_out.p)) || (cache && (!k.p || !slots || !kc || !ks || (v.p && (!vc || !vs)))) ||
+      (axes > 0 && (!rotation->positions || !rotation->freqs)))
+    return KQ_ERR_NULL;
+  if (!aligned(q.p, 16) || !aligned(q_out.p, 16) || !aligned(k.p, 16) || !aligned(v.p, 16) || !aligned(slots, 4) ||
+      !aligned(kc, 16) || !aligned(ks, 4) || (v.p && (!aligned(vc, 16) || !aligned(vs, 4))) || !aligned(q_weight, 4) ||
+      !aligned(k_weight, 4) || (axes > 0 && (!aligned(rotation->positions, 4) || !aligned(rotation->freqs, 8))))
+    return KQ_ERR_ALIGN;
+  const uint64_t nc = cache ? (uint64_t)n_slots * (uint64_t)(kv_heads * head_dim) / 2 : 0;
+  const bool in_place = q.p == q_out.p && q.stride == q_out.stride;  // a lane reads a piece before it writes it
+  const uint64_t weight = norm != KQ_NORM_NONE ? (uint64_t)head_dim * 4 : 0;
+  const Range pools[] = {{kc, nc}, {ks, nc / 16}, {v.p ? vc : nullptr, nc}, {v.p ? vs : nullptr, nc / 16}};
+  const Range ins[] = {q.range(tokens), k.range(tokens), v.range(tokens), {slots, cache ? (uint64_t)tokens * 4 : 0},
+                       {q_weight, weight}, {k_weight, weight},
+                       {axes > 0 ? rotation->positions : nullptr, (uint64_t)tokens * axes * 4},
+                       {axes > 0 ? rotation->freqs : nullptr, (uint64_t)turned * 4}};
+  const Range rows_out = q_out.range(tokens);
+  if (any_alias(pools, 4, ins, 8) || any_alias(&rows_out, 1, ins + 3, 5) || any_alias(&rows_out, 1, pools, 4))
+    return KQ_ERR_ALIAS;
+  if ((!in_place && rows_touch(q_out, q, tokens)) || rows_touch(q_out, k, tokens) || rows_touch(q_out, v, tokens))
+    return KQ_ERR_ALIAS;
+  kq::RopeArgs a{};
+  a.part[0] = {q.p, q.stride, const_cast<uint16_t*>(q_out.p), q_out.stride, nullptr, nullptr, q_weight, (int)q_heads, true};
+  if (cache && n_slots > 0) {
+    a.part[1] = {k.p, k.stride, nullptr, 0, kc, ks, k_weight, (int)kv_heads, true};
+    a.part[2] = {v.p, v.stride, nullptr, 0, vc, vs, nullptr, v.p ? (int)kv_heads : 0, false};
+  } else if (q_heads == 0) {
+    return KQ_OK;
+  }
+  a.tokens = tokens;
+  a.head_dim = (int)head_dim;
+  a.norm = norm == KQ_NORM_RMS;
+  a.eps = (double)eps;
+  a.n_axes = axes;
+  for (int i = 0, end = 0; i < axes; ++i) a.axis_end[i] = end += rotation->axis_dims[i] / 2;
+  a.pairs = (int)(turned / 2);
+  if (axes > 0) {
+    a.positions = rotation->positions;
+    a.freqs = rotation->freqs;
+    a.halves = rotation->layout == KQ_ROPE_HALVES;
+  }
+  a.slots = slots;
+  a.n_slots = (int)n_slots;
+  return from_hip(kq::launch_rope(a, stream));
 }
 
 // Whether kq_gemm_mx_ex takes the few-row form: its time goes with the outputs, as the tile form's does not while its
@@ -606,6 +694,98 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
                         uint16_t* K, int64_t K_stride, uint16_t* V, int64_t V_stride, hipStream_t stream) {
   return run_cache(false, K, K_stride, V, V_stride, tokens, width, slots, n_slots, K_codes, K_scales, V_codes,
                    V_scales, stream);
+}
+
+kq_status kq_rope(const uint16_t* X, int64_t X_stride, int64_t tokens, int64_t heads, int64_t head_dim, kq_norm norm,
+                  const float* weight, float eps, const kq_rotation* rotation, uint16_t* out, int64_t out_stride,
+                  hipStream_t stream) {
+  if (heads <= 0 || heads > (int64_t(1) << 24)) return KQ_ERR_SHAPE;
+  const int64_t width = heads * head_dim;
+  return run_rope({X, X_stride, width}, heads, weight, {out, out_stride, width}, {}, {}, tokens, 0, head_dim, norm,
+                  nullptr, eps, rotation, nullptr, 0, nullptr, nullptr, nullptr, nullptr, stream);
+}
+
+kq_status kq_cache_write_rope(const uint16_t* Q, int64_t Q_stride, int64_t q_heads, const float* q_weight,
+                              uint16_t* Q_out, int64_t Q_out_stride, const uint16_t* K, int64_t K_stride,
+                              const uint16_t* V, int64_t V_stride, int64_t tokens, int64_t kv_heads, int64_t head_dim,
+                              kq_norm norm, const float* k_weight, float eps, const kq_rotation* rotation,
+                              const int32_t* slots, int64_t n_slots, uint8_t* K_codes, uint8_t* K_scales,
+                              uint8_t* V_codes, uint8_t* V_scales, hipStream_t stream) {
+  if (kv_heads <= 0 || kv_heads > (int64_t(1) << 24) || (Q && (q_heads <= 0 || q_heads > (int64_t(1) << 24))))
+    return KQ_ERR_SHAPE;
+  if (!Q) q_heads = 0;
+  const int64_t q_width = q_heads * head_dim, width = kv_heads * head_dim;
+  return run_rope({Q, Q_stride, q_width}, q_heads, Q ? q_weight : nullptr, {Q ? Q_out : nullptr, Q_out_stride, q_width},
+                  {K, K_stride, width}, {V, V_stride, width}, tokens, kv_heads, head_dim, norm, k_weight, eps, rotation,
+                  slots, n_slots, K_codes, K_scales, V_codes, V_scales, stream);
+}
+
+kq_status kq_residual_norm(const uint16_t* X, int64_t X_stride, const uint16_t* Y, int64_t Y_stride, int64_t tokens,
+                           int64_t d, kq_norm post, const float* post_weight, const float* gate, float residual_scale,
+                           uint16_t* X_out, int64_t X_out_stride, kq_norm pre, const float* pre_weight,
+                           const float* mod_scale, const float* mod_shift, int64_t tokens_per_sample, float eps,
+                           uint16_t* H, int64_t H_stride, uint8_t* out_codes, uint8_t* out_scales, float* row_stats,
+                           hipStream_t stream) {
+  const kq_status st = check_shape(tokens, d);
+  if (st != KQ_OK) return st;
+  const Rows x{X, X_stride, d}, y{Y, Y_stride, d}, out{X_out, X_out_stride, d}, h{H, H_stride, d};
+  for (const Rows* r : {&x, &y, &out, &h})
+    if (r->p && !good_stride(r->stride, d)) return KQ_ERR_SHAPE;
+  for (kq_norm n : {post, pre})
+    if (n != KQ_NORM_NONE && n != KQ_NORM_RMS && n != KQ_NORM_LAYER) return KQ_ERR_VARIANT;
+  if (!(eps >= 0.0f) || eps > 3.0e38f || !std::isfinite(residual_scale)) return KQ_ERR_SHAPE;
+  if ((gate || mod_scale || mod_shift) && tokens_per_sample <= 0) return KQ_ERR_SHAPE;
+  // without a block's output the stream is X as it is; statistics are those of a norm
+  if (!Y && (X_out || post != KQ_NORM_NONE || post_weight || gate || residual_scale != 1.0f)) return KQ_ERR_VARIANT;
+  if (row_stats && pre == KQ_NORM_NONE) return KQ_ERR_VARIANT;
+  if (tokens == 0) return KQ_OK;
+  if (!X || (Y && !X_out) || !out_codes != !out_scales || (!Y && !H && !out_codes && !row_stats)) return KQ_ERR_NULL;
+  if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(X_out, 16) || !aligned(H, 16) || !aligned(out_codes, 16) ||
+      !aligned(row_stats, 8))
+    return KQ_ERR_ALIGN;
+  for (const float* v : {post_weight, gate, pre_weight, mod_scale, mod_shift})
+    if (!aligned(v, 16)) return KQ_ERR_ALIGN;
+  const int64_t per = (gate || mod_scale || mod_shift) ? std::min(tokens_per_sample, tokens) : tokens;
+  const uint64_t n = (uint64_t)tokens * (uint64_t)d, row = (uint64_t)d * 4;
+  const uint64_t vectors = (uint64_t)((tokens + per - 1) / per) * row;
+  const Range outs[] = {out.range(tokens), h.range(tokens), {out_codes, n / 2}, {out_scales, n / 32},
+                        {row_stats, (uint64_t)tokens * 8}};
+  const Range ins[] = {x.range(tokens), y.range(tokens), {post_weight, row}, {gate, vectors},
+                       {pre_weight, row}, {mod_scale, vectors}, {mod_shift, vectors}};
+  // rows against rows may be columns of one matrix, and the stream may be updated in place
+  if (any_alias(outs + 2, 3, ins, 7)) return KQ_ERR_ALIAS;
+  for (int i = 0; i < 2; ++i)
+    if (any_alias(outs + i, 1, ins + 2, 5) || any_alias(outs + i, 1, outs + 2, 3)) return KQ_ERR_ALIAS;
+  const bool in_place = X == X_out && X_stride == X_out_stride;  // a lane reads a piece before it writes it
+  if ((!in_place && rows_touch(out, x, tokens)) || rows_touch(out, y, tokens) || rows_touch(out, h, tokens) ||
+      rows_touch(h, x, tokens) || rows_touch(h, y, tokens))
+    return KQ_ERR_ALIAS;
+  kq::NormArgs a{};
+  a.x = X;
+  a.y = Y;
+  a.x_out = X_out;
+  a.x_stride = X_stride;
+  a.y_stride = Y_stride;
+  a.x_out_stride = X_out_stride;
+  a.tokens = tokens;
+  a.d = (int)d;
+  a.post = (int)post;
+  a.pre = (int)pre;
+  a.post_w = post_weight;
+  a.gate = gate;
+  a.residual_scale = (double)residual_scale;
+  a.pre_w = pre_weight;
+  a.mod_scale = mod_scale;
+  a.mod_shift = mod_shift;
+  a.by_sample = kq::make_divisor((unsigned)per);
+  a.eps = (double)eps;
+  a.next = H || out_codes || row_stats;
+  a.h = H;
+  a.h_stride = H_stride;
+  a.codes = out_codes;
+  a.scales = out_scales;
+  a.stats = row_stats;
+  return from_hip(kq::launch_residual_norm(a, stream));
 }
 
 int64_t kq_attention_mx_workspace(int64_t q_rows, int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads,

@@ -155,6 +155,67 @@ struct CacheArgs {
   Divisor by_chunks;  // set by launch_cache
 };
 
+// Rows of heads, normalised and turned (kq_rope.hip).  Strides in elements.
+struct RopePart {  // queries (or any rows), keys or values of a call; heads 0: none
+  const uint16_t* x;
+  int64_t x_stride;
+  uint16_t* out;  // rows, or
+  int64_t out_stride;
+  uint8_t* codes;  // the pools of a cache (null: rows)
+  uint8_t* scales;
+  const float* weight;  // of the norm, [head_dim] (null: 1)
+  int heads;
+  bool turn;  // false: taken as they are (values)
+  // set by launch_rope: heads and lanes of a unit, tokens of a wave, units of a token, units of a wave, waves of a
+  // wave's tokens, waves in all
+  int unit_heads, lanes, tokens, units, per, chunks;
+  int64_t waves;
+};
+
+struct RopeArgs {
+  RopePart part[3];
+  int64_t tokens;
+  int head_dim;
+  bool norm;
+  double eps;
+  const int32_t* positions;  // [tokens][n_axes]
+  const double* freqs;       // [pairs]
+  int n_axes;                // 0: nothing turns
+  int axis_end[4];           // the pair after an axis' last
+  int pairs;
+  bool halves;
+  const int32_t* slots;
+  int n_slots;
+  // set by launch_rope
+  int64_t waves;
+  double inv_dim;
+};
+
+// The residual stream between two blocks (kq_norm.hip).  Strides in elements; norms 0 none, 1 RMS, 2 layer.
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* y;  // null: x is the stream already
+  uint16_t* x_out;
+  int64_t x_stride, y_stride, x_out_stride;
+  int64_t tokens;
+  int d;
+  int post, pre;
+  const float* post_w;
+  const float* gate;  // [samples][d]
+  double residual_scale;
+  const float* pre_w;
+  const float* mod_scale;  // [samples][d]
+  const float* mod_shift;
+  Divisor by_sample;  // rows of a sample
+  double eps;
+  bool next;    // any of the outputs below
+  uint16_t* h;  // may be null, as the others
+  int64_t h_stride;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* stats;
+};
+
 // Attention over the cache: see kq_attn.hip.  Strides in elements.
 struct AttnArgs {
   const uint16_t* q;
@@ -209,6 +270,8 @@ int64_t attn_workspace(int64_t q_rows, int64_t q_heads, int64_t head_dim, const 
 hipError_t launch_attn(const AttnArgs& args, hipStream_t stream);
 
 hipError_t launch_cache(bool write, bool both, const CacheArgs& args, hipStream_t stream);
+hipError_t launch_rope(const RopeArgs& args, hipStream_t stream);
+hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream);
 hipError_t launch_gemm(const GemmArgs& args, hipStream_t stream);
 // The same for few rows (kq_gemm_rows.hip).
 hipError_t launch_gemm_rows(const GemmArgs& args, hipStream_t stream);
