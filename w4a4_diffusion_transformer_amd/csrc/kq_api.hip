@@ -777,6 +777,7 @@ kq_status kq_residual_norm(const uint16_t* X, int64_t X_stride, const uint16_t* 
   a.pre_w = pre_weight;
   a.mod_scale = mod_scale;
   a.mod_shift = mod_shift;
+  a.sample_rows = per;
   a.by_sample = kq::make_divisor((unsigned)per);
   a.eps = (double)eps;
   a.next = H || out_codes || row_stats;

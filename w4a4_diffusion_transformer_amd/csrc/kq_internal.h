@@ -206,7 +206,8 @@ struct NormArgs {
   const float* pre_w;
   const float* mod_scale;  // [samples][d]
   const float* mod_shift;
-  Divisor by_sample;  // rows of a sample
+  int64_t sample_rows;  // rows of a sample
+  Divisor by_sample;
   double eps;
   bool next;    // any of the outputs below
   uint16_t* h;  // may be null, as the others
@@ -214,6 +215,9 @@ struct NormArgs {
   uint8_t* codes;
   uint8_t* scales;
   float* stats;
+  // set by launch_residual_norm: consecutive rows of a workgroup
+  int64_t group_rows;
+  double inv_d;
 };
 
 // Attention over the cache: see kq_attn.hip.  Strides in elements.

@@ -54,14 +54,6 @@ __device__ __forceinline__ void sincos_quarters(double x, double& s, double& c) 
   c = (quarter + 1) & 2 ? -b : b;
 }
 
-// 1 / sqrt(a): the estimate and two Newton steps; zero for infinite a.
-__device__ __forceinline__ double inverse_sqrt(double a) {
-  double y = __builtin_amdgcn_rsq(a);
-  y = fma(0.5 * y, fma(-a * y, y, 1.0), y);
-  y = fma(0.5 * y, fma(-a * y, y, 1.0), y);
-  return a < __builtin_huge_val() ? y : 1.0 / a;
-}
-
 __device__ __forceinline__ double from_lane(double v, int lane) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   const unsigned lo = (unsigned)__builtin_amdgcn_ds_bpermute(4 * lane, (int)(unsigned)b);

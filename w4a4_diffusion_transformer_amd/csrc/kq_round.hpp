@@ -31,8 +31,9 @@ __device__ __forceinline__ void piece_values(u32x4 v, double x[8]) {
 // 21 significant bits, so the conversion to fp32 is exact (above 2^-126).
 __device__ __forceinline__ float to_odd(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const unsigned lo = (unsigned)b, hi = (unsigned)(b >> 32) | (lo < 1u ? lo : 1u);
-  return (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
+  unsigned any;  // one instruction, where min(lo, 1) would be compiled to a comparison and a selection
+  asm("v_min_u32_e32 %0, 1, %1" : "=v"(any) : "v"((unsigned)b));
+  return (float)__builtin_bit_cast(double, (uint64_t)((unsigned)(b >> 32) | any) << 32);
 }
 
 // 8 values rounded once to bf16 (nearest even), packed.
@@ -56,34 +57,69 @@ __device__ __forceinline__ void quantize_piece(u32x4 v, unsigned& word, unsigned
   word = pack_fp4(y, byte);
 }
 
-template <int CTRL>
-__device__ __forceinline__ double dpp_add(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)b, CTRL, 0xF, 0xF, false);
-  const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), CTRL, 0xF, 0xF, false);
-  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+// 1 / sqrt(a): the estimate and two Newton steps (some 2^-52); the estimate itself where those do not apply (0 gives
+// infinity, infinity 0).
+__device__ __forceinline__ double inverse_sqrt(double a) {
+  const double e = __builtin_amdgcn_rsq(a);
+  double y = fma(0.5 * e, fma(-a * e, e, 1.0), e);
+  y = fma(0.5 * y, fma(-a * y, y, 1.0), y);
+  return a > 0.0 && a < __builtin_huge_val() ? y : e;
 }
 
-// Sum over each aligned group of 2^LOG lanes (LOG up to 6), in every lane: lanes 1 and 2 apart by quad
-// permutations, then mirrors of 8 and 16 lanes, then the swaps of 16 and 32 lanes.
+template <int CTRL>
+__device__ __forceinline__ double from_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const unsigned lo = (unsigned)__builtin_amdgcn_mov_dpp((int)(unsigned)b, CTRL, 0xF, 0xF, true);
+  const unsigned hi = (unsigned)__builtin_amdgcn_mov_dpp((int)(unsigned)(b >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Permutations within a row of 16 lanes.
+enum { DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_ROTATE4 = 0x124, DPP_ROTATE8 = 0x128, DPP_MIRROR8 = 0x141 };
+
+// v of this lane plus v of the lane 16 (32) away.
+__device__ __forceinline__ double add_swap16(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const auto lo = __builtin_amdgcn_permlane16_swap((unsigned)b, (unsigned)b, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
+  return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+}
+
+__device__ __forceinline__ double add_swap32(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const auto lo = __builtin_amdgcn_permlane32_swap((unsigned)b, (unsigned)b, false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
+  return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+}
+
+// Sum over each aligned group of 2^LOG lanes (LOG up to 4), in every lane.
 template <int LOG>
 __device__ __forceinline__ double group_sum(double v) {
-  if constexpr (LOG >= 1) v = dpp_add<0xB1>(v);
-  if constexpr (LOG >= 2) v = dpp_add<0x4E>(v);
-  if constexpr (LOG >= 3) v = dpp_add<0x141>(v);
-  if constexpr (LOG >= 4) v = dpp_add<0x140>(v);
-  if constexpr (LOG >= 5) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const auto lo = __builtin_amdgcn_permlane16_swap((unsigned)b, (unsigned)b, false, false);
-    const auto hi = __builtin_amdgcn_permlane16_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
-    v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  if constexpr (LOG >= 1) v += from_dpp<DPP_XOR1>(v);
+  if constexpr (LOG >= 2) v += from_dpp<DPP_XOR2>(v);
+  if constexpr (LOG == 3) v += from_dpp<DPP_MIRROR8>(v);  // quads are equal: the other one of 8 lanes
+  if constexpr (LOG >= 4) {
+    v += from_dpp<DPP_ROTATE4>(v);
+    v += from_dpp<DPP_ROTATE8>(v);
   }
-  if constexpr (LOG >= 6) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const auto lo = __builtin_amdgcn_permlane32_swap((unsigned)b, (unsigned)b, false, false);
-    const auto hi = __builtin_amdgcn_permlane32_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
-    v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  return v;
+}
+
+// Two sums over each aligned group of 2^LOG lanes (LOG 2 to 6) at the cost of one: after a first exchange even lanes
+// carry the first and odd lanes the second, and no later step mixes them.  Even lanes return the first sum.
+template <int LOG>
+__device__ __forceinline__ double group_sums(double s, double q) {
+  const bool odd = threadIdx.x & 1;
+  double v = (odd ? q : s) + from_dpp<DPP_XOR1>(odd ? s : q);
+  v += from_dpp<DPP_XOR2>(v);
+  if constexpr (LOG == 3) {  // the other quad by way of the mirror and the neighbour
+    v += from_dpp<DPP_XOR1>(from_dpp<DPP_MIRROR8>(v));
+  } else if constexpr (LOG >= 4) {
+    v += from_dpp<DPP_ROTATE4>(v);
+    v += from_dpp<DPP_ROTATE8>(v);
   }
+  if constexpr (LOG >= 5) v = add_swap16(v);
+  if constexpr (LOG >= 6) v = add_swap32(v);
   return v;
 }
 
