@@ -218,6 +218,41 @@ def test_rows_past_4_gib():
     assert not codes[:-2].any() and not scales[:-2].any()
 
 
+@pytest.mark.parametrize("d", [64, 1152])
+def test_rows_far_apart(d):
+    """Strides that no 32-bit offset spans over the rows of a wave, of one matrix and of all."""
+    tokens, stride = 1030, (1 << 25) + 8
+    flat = torch.zeros((tokens - 1) * stride + d, dtype=torch.bfloat16, device=DEV)
+    far = flat.as_strided((tokens, d), (stride, 1))
+    x, y = cref.bf16((tokens, d), 1), cref.bf16((tokens, d), 2)
+    far.copy_(x.to(DEV))
+    gate = vector((1, d), 3)
+    for out in (far, torch.empty((tokens, d), dtype=torch.bfloat16, device=DEV)):
+        far.copy_(x.to(DEV))
+        codes, scales = kq.alloc_outputs(y)
+        codes, scales = codes.to(DEV), scales.to(DEV)
+        kq.kq_residual_norm(far, y.to(DEV), out, post=1, pre=1, gate=gate.to(DEV), out_codes=codes, out_scales=scales)
+        stored = out.cpu()
+        ref.check(stored, *ref.residual(x, y, 1, gate=gate))
+        want, slack, *_ = ref.following(stored, 1)
+        lo, hi = ref.between(want, slack)
+        same = (lo == hi).view(tokens, -1, 32).all(2).all(1)  # rows without a tie
+        assert same.float().mean() > 0.99
+        ref.check_codes(codes.cpu()[same], scales.cpu()[same], lo[same].to(torch.bfloat16))
+    del flat, far
+
+
+# pieces a lane and rows a wave: the choices of the launch at many rows
+@pytest.mark.parametrize("tokens,d", [(5000, 32), (5003, 96), (4101, 160), (6000, 512), (5001, 736), (4099, 800), (3001, 1152),
+                                      (9001, 1152), (5001, 1536), (4100, 1760), (2051, 2240), (1100, 2592), (1100, 3040)])
+def test_many_rows(tokens, d):
+    g = torch.Generator().manual_seed(d)
+    x = (torch.randn((tokens, d), generator=g)).to(torch.bfloat16)
+    y = (torch.randn((tokens, d), generator=g) * 2).to(torch.bfloat16)
+    per = tokens // 3 + 1
+    run_and_check(x, y, per=per, post=1, pre=2, post_weight=vector(d, 1), gate=vector((3, d), 2), mod_shift=vector((3, d), 3))
+
+
 def test_no_rows():
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
     kq.kq_residual_norm(x, x, x, pre=1, h=x)

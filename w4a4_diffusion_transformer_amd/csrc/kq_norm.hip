@@ -21,6 +21,8 @@
 //          a wave, for few rows, and for samples of few rows;
 //   long   a row to a workgroup, read from memory again for each step.
 // In the first two each row of x and y is read once.
+#include <algorithm>
+
 #include "kq_device.hpp"
 #include "kq_internal.h"
 #include "kq_mxval.hpp"
@@ -33,41 +35,44 @@ namespace {
 typedef __attribute__((ext_vector_type(2))) double f64x2;
 
 constexpr int kMaxWaves = 16;
+constexpr int kMaxPieces = 6;      // of a lane of the rows kernel
+constexpr int kRowsThreads = 512;  // of its workgroups
 constexpr int kLong = 1024;  // threads of a workgroup whose rows stay in memory
 
-// A row, or a vector of a sample, by pieces.  UNIFORM: the same one for the whole wave, a buffer of its own: its
-// address stays in scalar registers, pieces past its end read as zero and are not written.  Else each lane has its
-// own, `there` or not.
-template <bool UNIFORM>
-struct Row {
-  __amdgpu_buffer_rsrc_t r;
-  __device__ Row(const void* base, int64_t bytes, bool) : r(rsrc_uniform(base, bytes)) {}
-  __device__ u32x4 load(int p) const { return __builtin_amdgcn_raw_buffer_load_b128(r, 16 * p, 0, kNT); }
-  __device__ void store(int p, u32x4 v) const { __builtin_amdgcn_raw_buffer_store_b128(v, r, 16 * p, 0, 0); }
-  __device__ void store_codes(int p, unsigned w) const { __builtin_amdgcn_raw_buffer_store_b32(w, r, 4 * p, 0, 0); }
-  __device__ void store_scale(int p, unsigned b) const {
-    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)b, r, p & 3 ? (int)kOut : p >> 2, 0, 0);
-  }
+// This lane's pieces of a wave's rows, P pieces `step` bytes apart: of one row, a buffer of its own (address in scalar
+// registers, pieces past its end read as zero and are not written), or with LOG < 6 of row `sub` of several rows
+// `stride` bytes apart in one buffer.  `there`: which lanes have their pieces but the last, and the last (LOG < 6).
+struct Lane {
+  int sub, piece;
+  bool there, last;
 };
 
-template <>
-struct Row<false> {
-  uint8_t* base;
-  int64_t bytes;  // 0: not there
-  __device__ Row(const void* b, int64_t n, bool there) : base((uint8_t*)b), bytes(there ? n : 0) {}
-  __device__ u32x4 load(int p) const {
-    u32x4 v{0, 0, 0, 0};
-    if (16 * p < bytes) v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + 16 * p));
-    return v;
+template <int LOG, int P>
+struct Rows {
+  __amdgpu_buffer_rsrc_t r;
+  int main, last;
+  // offset: of the lane's first piece in its row
+  __device__ Rows(const void* base, int64_t stride, int64_t bytes, const Lane& l, int offset)
+      : r(rsrc_uniform(base, bytes + (LOG < 6 ? ((64 >> LOG) - 1) * stride : 0))) {
+    main = last = offset;
+    if constexpr (LOG < 6) {
+      constexpr int kPast = (int)0x80000000u;  // and any step from it lie past every buffer
+      const int at = l.sub * (int)stride + offset;
+      main = l.there ? at : kPast;
+      last = l.last ? at : kPast;
+    }
   }
-  __device__ void store(int p, u32x4 v) const {
-    if (16 * p < bytes) *reinterpret_cast<u32x4*>(base + 16 * p) = v;
+  template <int STEP>
+  __device__ int offset(int k) const { return (k == P - 1 ? last : main) + k * STEP * (1 << LOG); }
+  __device__ u32x4 load(int k) const { return __builtin_amdgcn_raw_buffer_load_b128(r, offset<16>(k), 0, kNT); }
+  __device__ void store(int k, u32x4 v) const { __builtin_amdgcn_raw_buffer_store_b128(v, r, offset<16>(k), 0, 0); }
+  __device__ void store_codes(int k, unsigned w) const {
+    __builtin_amdgcn_raw_buffer_store_b32(w, r, offset<4>(k), 0, 0);
   }
-  __device__ void store_codes(int p, unsigned w) const {
-    if (4 * p < bytes) *reinterpret_cast<unsigned*>(base + 4 * p) = w;
-  }
-  __device__ void store_scale(int p, unsigned b) const {
-    if ((p & 3) == 0 && p >> 2 < bytes) base[p >> 2] = (uint8_t)b;
+  // four lanes have a scale: `first` of them writes it
+  __device__ void store_scale(int k, unsigned b, bool first) const {
+    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)b, r, first ? (k == P - 1 ? last : main) + k * (1 << LOG) / 4 : (int)kOut,
+                                         0, 0);
   }
 };
 
@@ -138,20 +143,21 @@ __device__ __forceinline__ u32x4 add_block(const NormArgs& a, u32x4 x, u32x4 y, 
   return round_piece(u);
 }
 
-template <bool UNIFORM>
+// Piece k of this lane of h, in rows from `first` on.
+template <int LOG, int P>
 __device__ __forceinline__ void store_next(const NormArgs& a, u32x4 x, const Norm& n, const double f[8], const double t[8],
-                                           int64_t row, int p, bool there) {
+                                           int64_t first, const Lane& l, int k) {
   double h[8];
   piece_values(x, h);
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = fma(fma(h[j], n.rstd, n.shift), f[j], t[j]);
   const u32x4 v = round_piece(h);
-  if (a.h) Row<UNIFORM>(a.h + row * a.h_stride, 2 * a.d, there).store(p, v);
+  if (a.h) Rows<LOG, P>(a.h + first * a.h_stride, 2 * a.h_stride, 2 * a.d, l, 16 * l.piece).store(k, v);
   if (a.codes) {
     unsigned word, byte;
     quantize_piece(v, word, byte);
-    Row<UNIFORM>(a.codes + row * (a.d >> 1), a.d >> 1, there).store_codes(p, word);
-    Row<UNIFORM>(a.scales + row * (a.d >> 5), a.d >> 5, there).store_scale(p, byte);
+    Rows<LOG, P>(a.codes + first * (a.d >> 1), a.d >> 1, a.d >> 1, l, 4 * l.piece).store_codes(k, word);
+    Rows<LOG, P>(a.scales + first * (a.d >> 5), a.d >> 5, a.d >> 5, l, l.piece >> 2).store_scale(k, byte, (l.piece & 3) == 0);
   }
 }
 
@@ -179,23 +185,26 @@ struct WaveSum {
   }
 };
 
-// The same over the waves of a workgroup, through LDS; two buffers in turn, so that one barrier parts a sum's writes
-// from its reads and its reads from the next writes.
+// The same over the waves of a workgroup, through LDS: a wave's two sums go to two neighbouring words, and each wave
+// adds up the words as lanes of its own.  Two buffers in turn, so that one barrier parts a sum's writes from its reads
+// and its reads from the next writes.
 struct WorkgroupSum {
   double (*red)[2 * kMaxWaves];
   int waves, turn = 0;
   __device__ __forceinline__ void operator()(double& s, double& q) {
-    const double v = group_sums<6>(s, q);
+    double v = group_sums<6>(s, q);
     const unsigned lane = threadIdx.x & 63;
     if (lane < 2) red[turn][2 * (threadIdx.x >> 6) + lane] = v;
     __syncthreads();
-    s = q = 0.0;
-#pragma unroll 1
-    for (int i = 0; i < waves; ++i) {
-      s += red[turn][2 * i];
-      q += red[turn][2 * i + 1];
-    }
+    v = 0.0;
+    if (lane < 2 * (unsigned)waves) v = red[turn][lane];
     turn ^= 1;
+    v += from_dpp<DPP_XOR2>(v);  // 32 words
+    v += from_dpp<DPP_ROTATE4>(v);
+    v += from_dpp<DPP_ROTATE8>(v);
+    v = add_swap16(v);
+    s = WaveSum<6>::from_first<0>(v);
+    q = WaveSum<6>::from_first<1>(v);
   }
 };
 
@@ -224,11 +233,11 @@ __device__ __forceinline__ Norm settle(const NormArgs& a, int kind, double s, do
   return n;
 }
 
-// A row of 2^LOG lanes with P pieces each (P > 1: LOG = 6).
+// A row of 2^LOG lanes with P pieces each.
 template <int LOG, int P, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
   constexpr int kLanes = 1 << LOG, kRows = 64 >> LOG, kPieces = kLanes * P;
-  constexpr bool UNIFORM = LOG == 6;
+  constexpr int kStep = THREADS / 64 * kRows;  // rows of the workgroup's waves
   // the folded vectors, two channels of each piece at a time: lanes read whole lines
   __shared__ f64x2 vectors[3][4][kPieces];
   const int pieces = a.d >> 3;
@@ -236,6 +245,7 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t row0 = (int64_t)blockIdx.x * a.group_rows;
   const int64_t row1 = row0 + a.group_rows < a.tokens ? row0 + a.group_rows : a.tokens;
+  const bool last_there = lane + kLanes * (P - 1) < pieces;  // of a lane's pieces only the last may be past the row
   auto vector = [&](int which, int p, double f[8]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -249,9 +259,24 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
     for (int k = 0; k < P; ++k) asm volatile("" : "+v"(v[k]));
   };
   WaveSum<LOG> sum;
+  constexpr bool kAhead = P <= 3;  // the next row's loads in flight, where registers allow it with four waves a SIMD
   for (int64_t first = row0; first < row1;) {
     const int64_t sample = fast_div((unsigned)first, a.by_sample);
     const int64_t end = (sample + 1) * a.sample_rows < row1 ? (sample + 1) * a.sample_rows : row1;
+    u32x4 nx[P], ny[P];
+    auto load = [&](int64_t at, u32x4* x, u32x4* y) {
+      const int64_t row = at < end ? at : end - 1;  // a wave without a row
+      const Lane l{sub, lane, at + sub < end, at + sub < end && last_there};
+      const Rows<LOG, P> xs(a.x + row * a.x_stride, 2 * a.x_stride, 2 * a.d, l, 16 * lane);
+#pragma unroll
+      for (int k = 0; k < P; ++k) x[k] = xs.load(k);
+      if (a.y) {
+        const Rows<LOG, P> ys(a.y + row * a.y_stride, 2 * a.y_stride, 2 * a.d, l, 16 * lane);
+#pragma unroll
+        for (int k = 0; k < P; ++k) y[k] = ys.load(k);
+      }
+    };
+    if (kAhead) load(first + wave * kRows, nx, ny);
     if (first > row0) __syncthreads();
     for (int p = threadIdx.x; p < pieces; p += THREADS) {
       Vectors v;
@@ -266,17 +291,18 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
         for (int j = 0; j < 4; ++j) vectors[i][j][p] = f64x2{f[i][2 * j], f[i][2 * j + 1]};
     }
     __syncthreads();
-    for (int64_t at = first + wave * kRows; at < end; at += THREADS / 64 * kRows) {
-      const bool there = at + sub < end;
-      const int64_t row = there ? at + sub : end - 1;
+    for (int64_t at = first + wave * kRows; at < end; at += kStep) {
+      const Lane l{sub, lane, at + sub < end, at + sub < end && last_there};
       u32x4 x[P], y[P];
-      const Row<UNIFORM> xs(a.x + row * a.x_stride, 2 * a.d, true);
+      if constexpr (kAhead) {
 #pragma unroll
-      for (int k = 0; k < P; ++k) x[k] = xs.load(lane + kLanes * k);
-      if (a.y) {
-        const Row<UNIFORM> ys(a.y + row * a.y_stride, 2 * a.d, true);
-#pragma unroll
-        for (int k = 0; k < P; ++k) y[k] = ys.load(lane + kLanes * k);
+        for (int k = 0; k < P; ++k) {
+          x[k] = nx[k];
+          y[k] = ny[k];
+        }
+        if (at + kStep < end) load(at + kStep, nx, ny);
+      } else {
+        load(at, x, y);
       }
       auto moments = [&](const u32x4* v, double& s, double& q) {
         s = q = 0.0;
@@ -292,7 +318,7 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
         return [=](auto&& use) {
 #pragma unroll
           for (int k = 0; k < P; ++k)
-            if (lane + kLanes * k < pieces) use(v[k]);
+            if (k < P - 1 || last_there) use(v[k]);
         };
       };
       Norm n;
@@ -304,15 +330,15 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
           n = settle(a, a.post, s, q, sum, pieces_of(y));
           again(y);
         }
-        const Row<UNIFORM> out(a.x_out + row * a.x_out_stride, 2 * a.d, there);
+        const Rows<LOG, P> out(a.x_out + at * a.x_out_stride, 2 * a.x_out_stride, 2 * a.d, l, 16 * lane);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           const int p = lane + kLanes * k;
           double f[8];
           vector(0, p, f);
           x[k] = add_block(a, x[k], y[k], n, f);
-          out.store(p, x[k]);
-          if (p >= pieces) x[k] = u32x4{0, 0, 0, 0};
+          out.store(k, x[k]);
+          if (k == P - 1 && !last_there) x[k] = u32x4{0, 0, 0, 0};
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -331,13 +357,13 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
           double f[8], t[8];
           vector(1, p, f);
           vector(2, p, t);
-          store_next<UNIFORM>(a, x[k], n, f, t, row, p, there);
+          store_next<LOG, P>(a, x[k], n, f, t, at, l, k);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if (a.stats && lane == 0 && there) {
-        a.stats[2 * row] = (float)n.mean;
-        a.stats[2 * row + 1] = (float)n.rstd;
+      if (a.stats && lane == 0 && at + sub < end) {
+        a.stats[2 * (at + sub)] = (float)n.mean;
+        a.stats[2 * (at + sub) + 1] = (float)n.rstd;
       }
     }
     first = end;
@@ -356,13 +382,14 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
 
   u32x4 nx[P], ny[P];
   auto load = [&](int64_t row) {
-    const Row<true> xs(a.x + row * a.x_stride, 2 * a.d, true);
+    auto piece = [&](const uint16_t* base, int k) {
+      return Rows<6, 1>(base, 0, 2 * a.d, Lane{}, 16 * (lane + lanes * k)).load(0);
+    };
 #pragma unroll
-    for (int k = 0; k < P; ++k) nx[k] = xs.load(lane + lanes * k);
+    for (int k = 0; k < P; ++k) nx[k] = piece(a.x + row * a.x_stride, k);
     if (a.y) {
-      const Row<true> ys(a.y + row * a.y_stride, 2 * a.d, true);
 #pragma unroll
-      for (int k = 0; k < P; ++k) ny[k] = ys.load(lane + lanes * k);
+      for (int k = 0; k < P; ++k) ny[k] = piece(a.y + row * a.y_stride, k);
     }
   };
   auto again = [](u32x4* v) {
@@ -418,7 +445,6 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
         n = settle(a, a.post, s, q, sum, pieces_of(y));
         again(y);
       }
-      const Row<true> out(a.x_out + row * a.x_out_stride, 2 * a.d, true);
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         const int p = lane + lanes * k;
@@ -428,7 +454,7 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
           block_factor(v, f[0]);
         }
         x[k] = add_block(a, x[k], y[k], n, f[KEEP ? k : 0]);
-        out.store(p, x[k]);
+        Rows<6, 1>(a.x_out + row * a.x_out_stride, 0, 2 * a.d, Lane{}, 16 * p).store(0, x[k]);
         if (p >= pieces) x[k] = u32x4{0, 0, 0, 0};
       }
     }
@@ -449,7 +475,7 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
           load_next_vectors(a, sample, p, v);
           next_factor(v, nf[0], nt[0]);
         }
-        store_next<true>(a, x[k], n, nf[KEEP ? k : 0], nt[KEEP ? k : 0], row, p, true);
+        store_next<6, 1>(a, x[k], n, nf[KEEP ? k : 0], nt[KEEP ? k : 0], row, Lane{0, p}, 0);
       }
     }
     if (a.stats && lane == 0) {
@@ -513,7 +539,7 @@ __global__ __launch_bounds__(kLong) void long_rows_kernel(NormArgs a) {
         load_next_vectors(a, sample, i, w);
         double f[8], t[8];
         next_factor(w, f, t);
-        store_next<true>(a, *(reinterpret_cast<const u32x4*>(stream + row * stride) + i), n, f, t, row, i, true);
+        store_next<6, 1>(a, *(reinterpret_cast<const u32x4*>(stream + row * stride) + i), n, f, t, row, Lane{0, i}, 0);
       }
     }
     if (a.stats && threadIdx.x == 0) {
@@ -523,11 +549,21 @@ __global__ __launch_bounds__(kLong) void long_rows_kernel(NormArgs a) {
   }
 }
 
+#define KQ_ROWS(LOG)                                                                                            \
+  {(const void*)&rows_kernel<LOG, 1, kRowsThreads>, (const void*)&rows_kernel<LOG, 2, kRowsThreads>,            \
+   (const void*)&rows_kernel<LOG, 3, kRowsThreads>, (const void*)&rows_kernel<LOG, 4, kRowsThreads>,            \
+   (const void*)&rows_kernel<LOG, 5, kRowsThreads>, (const void*)&rows_kernel<LOG, 6, kRowsThreads>}
+const void* const rows_kernels[5][kMaxPieces] = {KQ_ROWS(2), KQ_ROWS(3), KQ_ROWS(4), KQ_ROWS(5), KQ_ROWS(6)};
+#undef KQ_ROWS
+
 }  // namespace
 
 hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
   NormArgs a = args;
   a.inv_d = 1.0 / a.d;
+  // strides past what offsets between the rows of a wave hold
+  const int64_t most = std::max({a.x_stride, a.y ? a.y_stride : 0, a.y ? a.x_out_stride : 0, a.h ? a.h_stride : 0});
+  const bool far = most > int64_t(1) << 25;
   const int64_t pieces = a.d / 8, cus = cu_count();
   void* kargs[] = {&a};
   if (pieces > 128 * kMaxWaves) {
@@ -537,19 +573,25 @@ hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
   }
   const void* fn;
   int threads;
-  int64_t rows, slots;  // rows of a step of a workgroup; workgroups that run at once
-  if (pieces <= 64 || (pieces <= 384 && a.tokens > 4 * cus && a.sample_rows >= 64)) {
-    static const void* const narrow[] = {(const void*)&rows_kernel<2, 1, 512>, (const void*)&rows_kernel<3, 1, 512>,
-                                         (const void*)&rows_kernel<4, 1, 512>, (const void*)&rows_kernel<5, 1, 512>};
-    static const void* const whole[] = {(const void*)&rows_kernel<6, 1, 512>, (const void*)&rows_kernel<6, 2, 512>,
-                                        (const void*)&rows_kernel<6, 3, 512>, (const void*)&rows_kernel<6, 4, 512>,
-                                        (const void*)&rows_kernel<6, 5, 512>, (const void*)&rows_kernel<6, 6, 512>};
-    int log = 2;
-    while (log < 6 && (1 << log) < pieces) ++log;
-    const int64_t per = (pieces + 63) / 64;
-    fn = log < 6 ? narrow[log - 2] : whole[per - 1];
-    threads = 512;
-    rows = threads >> log;
+  int64_t rows, slots;  // rows of a step of a wave; workgroups that run at once
+  if (pieces <= 64 || (pieces <= 64 * kMaxPieces && a.tokens > 4 * cus && a.sample_rows >= 64)) {
+    // The fewest instructions: some 225 a piece of a lane and 120 for a row's sums, for all rows of a wave, and of
+    // waves as many as run at once do in one turn.  8192 rows of 1152: 2 rows a wave with 5 pieces TODO
+    int log = 6;
+    double best = 0.0;
+    for (int l = 6; l >= 2; --l) {
+      const int64_t per = (pieces + (1 << l) - 1) >> l;
+      if (per > kMaxPieces || (l < 6 && far)) break;
+      const double turns = (double)a.tokens / (double)((64 >> l) * 16 * cus);
+      const double cost = (turns > 1.0 ? turns : 1.0) * (double)(225 * per + 120);
+      if (l == 6 || cost < best) {
+        log = l;
+        best = cost;
+      }
+    }
+    fn = rows_kernels[log - 2][((pieces + (1 << log) - 1) >> log) - 1];
+    threads = kRowsThreads;
+    rows = 64 >> log;
     slots = cus * resident_per_cu(fn, threads);
   } else {
     const int64_t per = pieces <= 64 * kMaxWaves ? 1 : 2;
@@ -563,8 +605,8 @@ hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
     const int64_t room = 16 / ((waves + 3) / 4 * 4);
     slots = cus * (room > 1 ? room : 1);
   }
-  const int64_t steps = (a.tokens + rows - 1) / rows;
-  a.group_rows = (steps + slots - 1) / slots * rows;
+  // the same number of rows, of whole waves, for each workgroup that runs at once
+  a.group_rows = ((a.tokens + slots - 1) / slots + rows - 1) / rows * rows;
   const int64_t groups = (a.tokens + a.group_rows - 1) / a.group_rows;
   return hipLaunchKernel(fn, dim3((unsigned)groups), dim3(threads), kargs, 0, stream);
 }
