@@ -34,6 +34,10 @@ namespace {
 
 typedef __attribute__((ext_vector_type(2))) double f64x2;
 
+// Which of h and codes a kernel writes.  Where the next row's loads are in flight it has to be known when compiling:
+// with stores that may or may not be issued behind them, the wait for those loads is one for the stores too.
+enum { OUT_ROWS = 1, OUT_CODES = 2, OUT_ANY = 4 };
+
 constexpr int kMaxWaves = 16;
 constexpr int kMaxPieces = 6;      // of a lane of the rows kernel
 constexpr int kRowsThreads = 512;  // of its workgroups
@@ -121,11 +125,12 @@ __device__ __forceinline__ void block_factor(const Vectors& v, double f[8]) {
   for (int j = 0; j < 8; ++j) f[j] = (double)v.post_w[j >> 2][j & 3] * (double)v.gate[j >> 2][j & 3];
 }
 
-__device__ __forceinline__ void next_factor(const Vectors& v, double f[8], double t[8]) {
+template <class T>
+__device__ __forceinline__ void next_factor(const Vectors& v, double f[8], T t[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     f[j] = (double)v.pre_w[j >> 2][j & 3] * ((double)v.scale[j >> 2][j & 3] + 1.0);
-    t[j] = (double)v.shift[j >> 2][j & 3];
+    t[j] = (T)v.shift[j >> 2][j & 3];
   }
 }
 
@@ -144,16 +149,17 @@ __device__ __forceinline__ u32x4 add_block(const NormArgs& a, u32x4 x, u32x4 y, 
 }
 
 // Piece k of this lane of h, in rows from `first` on.
-template <int LOG, int P>
-__device__ __forceinline__ void store_next(const NormArgs& a, u32x4 x, const Norm& n, const double f[8], const double t[8],
+template <int LOG, int P, int OUT = OUT_ANY, class T>
+__device__ __forceinline__ void store_next(const NormArgs& a, u32x4 x, const Norm& n, const double f[8], const T t[8],
                                            int64_t first, const Lane& l, int k) {
   double h[8];
   piece_values(x, h);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = fma(fma(h[j], n.rstd, n.shift), f[j], t[j]);
+  for (int j = 0; j < 8; ++j) h[j] = fma(fma(h[j], n.rstd, n.shift), f[j], (double)t[j]);
   const u32x4 v = round_piece(h);
-  if (a.h) Rows<LOG, P>(a.h + first * a.h_stride, 2 * a.h_stride, 2 * a.d, l, 16 * l.piece).store(k, v);
-  if (a.codes) {
+  if (OUT == OUT_ANY ? a.h != nullptr : (OUT & OUT_ROWS) != 0)
+    Rows<LOG, P>(a.h + first * a.h_stride, 2 * a.h_stride, 2 * a.d, l, 16 * l.piece).store(k, v);
+  if (OUT == OUT_ANY ? a.codes != nullptr : (OUT & OUT_CODES) != 0) {
     unsigned word, byte;
     quantize_piece(v, word, byte);
     Rows<LOG, P>(a.codes + first * (a.d >> 1), a.d >> 1, a.d >> 1, l, 4 * l.piece).store_codes(k, word);
@@ -259,24 +265,9 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
     for (int k = 0; k < P; ++k) asm volatile("" : "+v"(v[k]));
   };
   WaveSum<LOG> sum;
-  constexpr bool kAhead = P <= 3;  // the next row's loads in flight, where registers allow it with four waves a SIMD
   for (int64_t first = row0; first < row1;) {
     const int64_t sample = fast_div((unsigned)first, a.by_sample);
     const int64_t end = (sample + 1) * a.sample_rows < row1 ? (sample + 1) * a.sample_rows : row1;
-    u32x4 nx[P], ny[P];
-    auto load = [&](int64_t at, u32x4* x, u32x4* y) {
-      const int64_t row = at < end ? at : end - 1;  // a wave without a row
-      const Lane l{sub, lane, at + sub < end, at + sub < end && last_there};
-      const Rows<LOG, P> xs(a.x + row * a.x_stride, 2 * a.x_stride, 2 * a.d, l, 16 * lane);
-#pragma unroll
-      for (int k = 0; k < P; ++k) x[k] = xs.load(k);
-      if (a.y) {
-        const Rows<LOG, P> ys(a.y + row * a.y_stride, 2 * a.y_stride, 2 * a.d, l, 16 * lane);
-#pragma unroll
-        for (int k = 0; k < P; ++k) y[k] = ys.load(k);
-      }
-    };
-    if (kAhead) load(first + wave * kRows, nx, ny);
     if (first > row0) __syncthreads();
     for (int p = threadIdx.x; p < pieces; p += THREADS) {
       Vectors v;
@@ -294,15 +285,13 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
     for (int64_t at = first + wave * kRows; at < end; at += kStep) {
       const Lane l{sub, lane, at + sub < end, at + sub < end && last_there};
       u32x4 x[P], y[P];
-      if constexpr (kAhead) {
+      const Rows<LOG, P> xs(a.x + at * a.x_stride, 2 * a.x_stride, 2 * a.d, l, 16 * lane);
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          x[k] = nx[k];
-          y[k] = ny[k];
-        }
-        if (at + kStep < end) load(at + kStep, nx, ny);
-      } else {
-        load(at, x, y);
+      for (int k = 0; k < P; ++k) x[k] = xs.load(k);
+      if (a.y) {
+        const Rows<LOG, P> ys(a.y + at * a.y_stride, 2 * a.y_stride, 2 * a.d, l, 16 * lane);
+#pragma unroll
+        for (int k = 0; k < P; ++k) y[k] = ys.load(k);
       }
       auto moments = [&](const u32x4* v, double& s, double& q) {
         s = q = 0.0;
@@ -371,7 +360,8 @@ __global__ __launch_bounds__(THREADS, 4) void rows_kernel(NormArgs a) {
 }
 
 // A row to a workgroup, P pieces a lane; KEEP: the folded vectors stay in registers.
-template <int P, bool KEEP, int THREADS>
+// Y: there is a block's output; OUT: of h and codes, what is written.
+template <int P, bool KEEP, int THREADS, bool Y, int OUT>
 __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
   __shared__ double red[2][2 * kMaxWaves];
   const int lane = threadIdx.x, lanes = blockDim.x;
@@ -387,7 +377,7 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
     };
 #pragma unroll
     for (int k = 0; k < P; ++k) nx[k] = piece(a.x + row * a.x_stride, k);
-    if (a.y) {
+    if constexpr (Y) {
 #pragma unroll
       for (int k = 0; k < P; ++k) ny[k] = piece(a.y + row * a.y_stride, k);
     }
@@ -396,7 +386,8 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < P; ++k) asm volatile("" : "+v"(v[k]));
   };
-  double f[KEEP ? P : 1][8], nf[KEEP ? P : 1][8], nt[KEEP ? P : 1][8];
+  double f[KEEP ? P : 1][8], nf[KEEP ? P : 1][8];
+  float nt[KEEP ? P : 1][8];
   int64_t sample_of_vectors = -1;
   if (row0 < row1) load(row0);
   for (int64_t row = row0; row < row1; ++row) {
@@ -438,7 +429,7 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
     };
     Norm n;
     double s, q;
-    if (a.y) {
+    if constexpr (Y) {
       if (a.post) {
         moments(y, s, q);
         again(y);
@@ -466,7 +457,7 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
       n = settle(a, a.pre, s, q, sum, pieces_of(x));
       again(x);
     }
-    if (a.h || a.codes) {
+    if constexpr (OUT != 0) {
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         const int p = lane + lanes * k;
@@ -475,7 +466,7 @@ __global__ __launch_bounds__(THREADS) void wide_kernel(NormArgs a) {
           load_next_vectors(a, sample, p, v);
           next_factor(v, nf[0], nt[0]);
         }
-        store_next<6, 1>(a, x[k], n, nf[KEEP ? k : 0], nt[KEEP ? k : 0], row, Lane{0, p}, 0);
+        store_next<6, 1, OUT>(a, x[k], n, nf[KEEP ? k : 0], nt[KEEP ? k : 0], row, Lane{0, p}, 0);
       }
     }
     if (a.stats && lane == 0) {
@@ -555,6 +546,14 @@ __global__ __launch_bounds__(kLong) void long_rows_kernel(NormArgs a) {
    (const void*)&rows_kernel<LOG, 5, kRowsThreads>, (const void*)&rows_kernel<LOG, 6, kRowsThreads>}
 const void* const rows_kernels[5][kMaxPieces] = {KQ_ROWS(2), KQ_ROWS(3), KQ_ROWS(4), KQ_ROWS(5), KQ_ROWS(6)};
 #undef KQ_ROWS
+#define KQ_WIDE(P, KEEP, THREADS, Y)                                                                            \
+  {(const void*)&wide_kernel<P, KEEP, THREADS, Y, 0>, (const void*)&wide_kernel<P, KEEP, THREADS, Y, OUT_ROWS>, \
+   (const void*)&wide_kernel<P, KEEP, THREADS, Y, OUT_CODES>,                                                   \
+   (const void*)&wide_kernel<P, KEEP, THREADS, Y, OUT_ROWS | OUT_CODES>}
+const void* const wide_kernels[3][2][4] = {{KQ_WIDE(1, true, 1024, false), KQ_WIDE(1, true, 1024, true)},
+                                           {KQ_WIDE(2, true, 768, false), KQ_WIDE(2, true, 768, true)},
+                                           {KQ_WIDE(2, false, 1024, false), KQ_WIDE(2, false, 1024, true)}};
+#undef KQ_WIDE
 
 }  // namespace
 
@@ -597,9 +596,7 @@ hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
     const int64_t per = pieces <= 64 * kMaxWaves ? 1 : 2;
     const int64_t waves = (pieces + 64 * per - 1) / (64 * per);
     threads = (int)(64 * waves);
-    fn = per == 1         ? (const void*)&wide_kernel<1, true, 1024>
-         : threads <= 768 ? (const void*)&wide_kernel<2, true, 768>
-                          : (const void*)&wide_kernel<2, false, 1024>;
+    fn = wide_kernels[per == 1 ? 0 : threads <= 768 ? 1 : 2][a.y != nullptr][(a.h ? OUT_ROWS : 0) | (a.codes ? OUT_CODES : 0)];
     rows = 1;
     // workgroups are dealt to the four SIMDs of a compute unit from the first on: 5 waves take the room of 8
     const int64_t room = 16 / ((waves + 3) / 4 * 4);
