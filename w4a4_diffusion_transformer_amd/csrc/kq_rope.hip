@@ -10,11 +10,18 @@
 // Everything is fp64 up to one rounding to bf16; keys are then quantized from
 // that bf16 as kq_cache_write does.
 //
-// Layout.  A lane holds one 8-channel piece (16 bytes) of a head.  A unit is
+// Layout.  A lane holds 8 channels of a head: four whole pairs, that is one
+// 16-byte piece where pairs are neighbours, two of 8 bytes, R/2 apart, where
+// they are halves, and the piece of its own where they do not turn.  A unit is
 // the fewest heads whose pieces are whole blocks of 32 (one head for rows that
 // are not quantized); a wave takes as many tokens as units fit its 64 lanes
 // and goes over the units of those tokens, so a lane's channels and position
-// never change and A and B are formed once.
+// never change and its cosines and sines, with the weights, are formed once.
+// Halves are brought back into pieces through the wave's own LDS before they
+// are quantized.  R that is no multiple of 8 takes a slower form: a lane holds
+// a piece and fetches each partner.
+#include <algorithm>
+
 #include "kq_device.hpp"
 #include "kq_internal.h"
 #include "kq_mxval.hpp"
@@ -27,7 +34,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // units whose loads a lane has in flight
 
-enum { ROT_NONE = 0, ROT_PAIRS = 1, ROT_SOME_PAIRS = 2, ROT_HALVES = 3 };
+// How pairs lie: not at all; neighbours or halves with R a multiple of 8; either with any R.
+enum { ROT_NONE = 0, ROT_PAIRS = 1, ROT_HALVES = 2, ROT_ANY_PAIRS = 3, ROT_ANY_HALVES = 4 };
 
 // sin and cos of x quarter turns: the nearest whole number of quarters comes off exactly (1.5 2^52 added and taken
 // away leaves it in the last bits), and the Taylor series on [-pi/4, pi/4] end below 2^-44.
@@ -89,11 +97,103 @@ __device__ __forceinline__ double head_sum(double v, int pieces, int first, int 
   return total;
 }
 
+// The sine and cosine of pair p at a token.
+__device__ __forceinline__ void turn_of(const RopeArgs& a, int64_t row, int p, double& sn, double& cs) {
+  int axis = 0;
+  for (int k = 0; k < a.n_axes - 1; ++k) axis += p >= a.axis_end[k];
+  sincos_quarters((double)a.positions[row * a.n_axes + axis] * (a.freqs[p] * 0.63661977236758134308), sn, cs);  // 2 / pi
+}
+
+// 1 / rms of the head that this lane's values are of.
+__device__ __forceinline__ double head_scale(const RopeArgs& a, const double y[8], int pieces, int first, int c) {
+  double q = 0.0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q = fma(y[j], y[j], q);
+  return inverse_sqrt(fma(head_sum(q, pieces, first, c), a.inv_dim, a.eps));
+}
+
+// Lanes with whole pairs: values j and partner(j) of a lane are a pair.
+template <int ROT>
+struct WholePairs {
+  static constexpr bool kHalves = ROT == ROT_HALVES;
+  double cu[4], sv[4], su[4], cv[4];  // cosine and sine times the weight of the first (u) or second (v) channel
+  bool turns;
+
+  static __device__ constexpr int first_of(int j) { return kHalves ? j : 2 * j; }
+  static __device__ constexpr int second_of(int j) { return kHalves ? 4 + j : 2 * j + 1; }
+
+  // lo, hi: the channels of the lane's first and last four values
+  __device__ __forceinline__ void form(const RopeArgs& a, int64_t row, const float* weight, int c, int lo, int hi) {
+    turns = ROT != ROT_NONE && 4 * c < a.pairs;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      double sn = 0.0, cs = 1.0;
+      if (ROT != ROT_NONE && turns) turn_of(a, row, 4 * c + j, sn, cs);
+      double wu = 1.0, wv = 1.0;
+      if (weight) {
+        wu = (double)weight[first_of(j) < 4 ? lo + first_of(j) : hi + first_of(j) - 4];
+        wv = (double)weight[second_of(j) < 4 ? lo + second_of(j) : hi + second_of(j) - 4];
+      }
+      cu[j] = wu * cs;
+      sv[j] = wv * sn;
+      su[j] = wu * sn;
+      cv[j] = wv * cs;
+    }
+  }
+  __device__ __forceinline__ void apply(double y[8], double r) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double u = y[first_of(j)], v = y[second_of(j)];
+      double nu = cu[j] * u, nv = cv[j] * v;
+      if (ROT != ROT_NONE && turns) {  // else the other channel may be infinite
+        nu = fma(-sv[j], v, nu);
+        nv = fma(su[j], u, nv);
+      }
+      y[first_of(j)] = nu * r;
+      y[second_of(j)] = nv * r;
+    }
+  }
+};
+
+// Lanes with one piece, of which any channels turn, with partners anywhere in the head.
+template <int ROT>
+struct AnyPairs {
+  double A[8], B[8];
+  int from[8];  // the partner's channel, or the channel itself
+  bool turns[8];
+
+  __device__ __forceinline__ void form(const RopeArgs& a, int64_t row, const float* weight, int c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int ch = 8 * c + j;
+      const bool upper = ROT == ROT_ANY_HALVES ? ch >= a.pairs : ch & 1;
+      const int pair = ROT == ROT_ANY_HALVES ? (upper ? ch - a.pairs : ch) : ch >> 1;
+      turns[j] = pair < a.pairs;
+      from[j] = !turns[j] ? ch : ROT == ROT_ANY_HALVES ? (upper ? pair : ch + a.pairs) : ch ^ 1;
+      double sn = 0.0, cs = 1.0;
+      if (turns[j]) turn_of(a, row, pair, sn, cs);
+      A[j] = weight ? cs * (double)weight[ch] : cs;
+      B[j] = (upper ? sn : -sn) * (weight ? (double)weight[from[j]] : 1.0);
+    }
+  }
+  // head: the raw channels of the head
+  __device__ __forceinline__ void apply(double y[8], double r, const uint16_t* head) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double other = turns[j] ? (double)__uint_as_float((unsigned)head[from[j]] << 16) : 0.0;
+      y[j] = fma(B[j], other, A[j] * y[j]) * r;
+    }
+  }
+};
+
 template <int ROT, bool NORM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
-  __shared__ u32x4 stage[ROT == ROT_HALVES ? kThreads : 1];
+  constexpr bool kAny = ROT >= ROT_ANY_PAIRS;
+  constexpr bool kStage = kAny || ROT == ROT_HALVES;
+  __shared__ u32x4 stage[kStage ? kThreads : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  u32x4* const mine = stage + (kStage ? 64 * wave : 0);
   const int pieces = a.head_dim >> 3;
   for (int64_t index = (int64_t)blockIdx.x * (kThreads / 64) + wave; index < a.waves;
        index += (int64_t)gridDim.x * (kThreads / 64)) {
@@ -104,130 +204,106 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     const int64_t tile = i / s.chunks;
     const int unit0 = (int)(i - tile * s.chunks) * s.per;
     const int unit1 = unit0 + s.per < s.units ? unit0 + s.per : s.units;
-    // this lane's token, head within a unit and piece within the head
+    // this lane's token, head within a unit and place within the head
     const int of_token = lane / s.lanes;
     const bool used = of_token < s.tokens;  // lanes past the last whole unit do as lane 0
     const int in_unit = used ? lane - of_token * s.lanes : 0;
     const int of_head = in_unit / pieces, c = in_unit - of_head * pieces;
     const int first = used ? lane - c : 0;  // the head's first lane
-    const int64_t t = tile * s.tokens + of_token;
+    const int64_t t0 = tile * s.tokens, t = t0 + (used ? of_token : 0);
     bool live = used && t < a.tokens;
-    const int64_t row = t < a.tokens ? t : a.tokens - 1;  // lanes without a token read one that is there
+    const int64_t row = t < a.tokens ? t : a.tokens - 1;
     const bool cache = s.codes != nullptr;
+    // channels of the first and the last four values
+    const bool apart = ROT == ROT_HALVES && s.turn && 4 * c < a.pairs;
+    const int lo = apart ? 4 * c : 8 * c, hi = apart ? a.pairs + 4 * c : 8 * c + 4;
+
+    // the rows of the wave's tokens are one buffer; heads are added as a scalar offset
+    const int64_t rows = t0 + s.tokens < a.tokens ? s.tokens : a.tokens - t0;
+    const auto rx = rsrc_uniform(s.x + t0 * s.x_stride, 2 * ((rows - 1) * s.x_stride + (int64_t)s.heads * a.head_dim));
+    const int of_row = 2 * ((int)(row - t0) * (int)s.x_stride + of_head * a.head_dim);
+    const int at_lo = of_row + 2 * lo, at_hi = of_row + 2 * hi;
+    auto load = [&](int unit) {
+      const int head = (unit < unit1 ? unit : unit1 - 1) * s.unit_heads * a.head_dim * 2;
+      if constexpr (ROT == ROT_HALVES) {
+        const u32x2 l = __builtin_amdgcn_raw_buffer_load_b64(rx, at_lo, head, 0);
+        const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(rx, at_hi, head, 0);
+        return u32x4{l[0], l[1], h[0], h[1]};
+      } else {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at_lo, head, 0));
+      }
+    };
+    u32x4 in[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) in[k] = load(unit0 + k);
+
     int64_t slot = 0;
     if (cache) {
       const int at = a.slots[row];
       live = live && (unsigned)at < (unsigned)a.n_slots;  // a token without a slot writes nothing
       slot = live ? at : 0;
     }
-    const uint16_t* const x = s.x + row * s.x_stride + 8 * c;
-
-    double A[8], B[8];
-    bool turns[8];
+    WholePairs<ROT> whole;
+    AnyPairs<ROT> any;
     if (s.turn) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int ch = 8 * c + j;
-        const bool upper = ROT == ROT_HALVES ? ch >= a.pairs : ch & 1;
-        const int pair = ROT == ROT_HALVES ? (upper ? ch - a.pairs : ch) : ch >> 1;
-        const bool turn = ROT != ROT_NONE && (ROT == ROT_PAIRS || pair < a.pairs);
-        turns[j] = turn;
-        A[j] = 1.0;
-        B[j] = 0.0;
-        if (turn) {
-          // two channels of an adjacent pair share their angle
-          if ((ROT == ROT_PAIRS || ROT == ROT_SOME_PAIRS) && (j & 1)) {
-            A[j] = A[j - 1];
-            B[j] = -B[j - 1];
-          } else {
-            int axis = 0;
-            for (int k = 0; k < a.n_axes - 1; ++k) axis += pair >= a.axis_end[k];
-            const double turned = a.freqs[pair] * 0.63661977236758134308;  // 2 / pi
-            double sn, cs;
-            sincos_quarters((double)a.positions[row * a.n_axes + axis] * turned, sn, cs);
-            A[j] = cs;
-            B[j] = upper ? sn : -sn;
-          }
-        }
-      }
-      if (NORM && s.weight) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int ch = 8 * c + j;
-          int partner = ch;
-          if constexpr (ROT == ROT_PAIRS || ROT == ROT_SOME_PAIRS) partner = ch ^ 1;
-          if constexpr (ROT == ROT_HALVES) partner = !turns[j] ? ch : ch >= a.pairs ? ch - a.pairs : ch + a.pairs;
-          A[j] *= (double)s.weight[ch];
-          B[j] *= (double)s.weight[partner];
-        }
-      }
+      const float* const weight = NORM ? s.weight : nullptr;
+      if constexpr (kAny) any.form(a, row, weight, c);
+      else whole.form(a, row, weight, c, lo, hi);
     }
+    uint8_t* const codes = s.codes + slot * (s.heads * pieces * 4) + 4 * in_unit;
+    uint8_t* const scales = s.scales + slot * (s.heads * pieces >> 2) + (in_unit >> 2);
+    const auto ro = rsrc_uniform(s.out + t0 * s.out_stride, 2 * ((rows - 1) * s.out_stride + (int64_t)s.heads * a.head_dim));
+    const int of_out = 2 * ((int)(row - t0) * (int)s.out_stride + of_head * a.head_dim);
+    const int out_lo = live ? of_out + 2 * lo : (int)kOut, out_hi = live ? of_out + 2 * hi : (int)kOut;
 
     for (int u0 = unit0; u0 < unit1; u0 += kBatch) {
-      u32x4 in[kBatch];
+      if (u0 > unit0) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        int head = (u0 + k) * s.unit_heads + of_head;
-        head = head < s.heads ? head : s.heads - 1;
-        in[k] = *reinterpret_cast<const u32x4*>(x + (int64_t)head * a.head_dim);
+        for (int k = 0; k < kBatch; ++k) in[k] = load(u0 + k);
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (u0 + k >= unit1) break;  // uniform
-        const int head = (u0 + k) * s.unit_heads + of_head;
         u32x4 v = in[k];
         if (s.turn) {
-          double y[8], other[8];
+          double y[8];
           piece_values(v, y);
-          if constexpr (ROT == ROT_PAIRS || ROT == ROT_SOME_PAIRS) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) other[j] = ROT == ROT_PAIRS || turns[j] ? y[j ^ 1] : 0.0;
-          } else if constexpr (ROT == ROT_HALVES) {
-            // the partners come through the wave's own LDS: a piece of them where halves are whole pieces
-            u32x4* const mine = stage + (threadIdx.x & ~63u);
+          double r = 1.0;
+          if constexpr (NORM) r = head_scale(a, y, pieces, first, c);
+          if constexpr (kAny) {
             mine[lane] = v;
             wave_lds_fence();
-            if ((a.pairs & 7) == 0) {
-              const int from = !turns[0] ? c : 8 * c >= a.pairs ? c - (a.pairs >> 3) : c + (a.pairs >> 3);
-              piece_values(mine[first + from], other);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) other[j] = turns[j] ? other[j] : 0.0;
-            } else {
-              const uint16_t* const head0 = reinterpret_cast<const uint16_t*>(mine + first);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int ch = 8 * c + j;
-                const int from = !turns[j] ? ch : ch >= a.pairs ? ch - a.pairs : ch + a.pairs;
-                other[j] = turns[j] ? (double)__uint_as_float((unsigned)head0[from] << 16) : 0.0;
-              }
-            }
+            any.apply(y, r, reinterpret_cast<const uint16_t*>(mine + first));
             wave_lds_fence();
-          }
-          double r = 1.0;
-          if constexpr (NORM) {
-            double q = 0.0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q = fma(y[j], y[j], q);
-            r = inverse_sqrt(fma(head_sum(q, pieces, first, c), a.inv_dim, a.eps));
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            y[j] *= A[j];
-            if constexpr (ROT != ROT_NONE) y[j] = fma(B[j], other[j], y[j]);
-            if constexpr (NORM) y[j] *= r;
+          } else {
+            whole.apply(y, r);
           }
           v = round_piece(y);
         }
+        const int unit = u0 + k;
         if (cache) {
+          if (ROT == ROT_HALVES && s.turn) {  // back into pieces
+            u32x2* const head = reinterpret_cast<u32x2*>(mine + first);
+            head[lo >> 2] = u32x2{v[0], v[1]};
+            head[hi >> 2] = u32x2{v[2], v[3]};
+            wave_lds_fence();
+            v = mine[lane];
+            wave_lds_fence();
+          }
           unsigned word, byte;
           quantize_piece(v, word, byte);
           if (live) {
-            const int chunk = head * pieces + c;
-            *reinterpret_cast<unsigned*>(s.codes + slot * (s.heads * pieces * 4) + 4 * chunk) = word;
-            if ((chunk & 3) == 0) s.scales[slot * (s.heads * pieces >> 2) + (chunk >> 2)] = (uint8_t)byte;
+            *reinterpret_cast<unsigned*>(codes + 4 * unit * s.lanes) = word;
+            if ((in_unit & 3) == 0) scales[unit * s.lanes >> 2] = (uint8_t)byte;
           }
-        } else if (live && head < s.heads) {
-          *reinterpret_cast<u32x4*>(s.out + row * s.out_stride + (int64_t)head * a.head_dim + 8 * c) = v;
+        } else {
+          const int head = unit * s.unit_heads * a.head_dim * 2;
+          if constexpr (ROT == ROT_HALVES) {
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, out_lo, head, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[2], v[3]}, ro, out_hi, head, 0);
+          } else {
+            __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_lo, head, 0);
+          }
         }
       }
     }
@@ -240,9 +316,10 @@ hipError_t launch_rope(const RopeArgs& args, hipStream_t stream) {
   RopeArgs a = args;
   a.inv_dim = 1.0 / a.head_dim;
   const int pieces = a.head_dim / 8;
+  const bool eights = a.pairs % 4 == 0;
   const int rot = a.n_axes == 0 ? ROT_NONE
-                  : a.halves    ? ROT_HALVES
-                  : 2 * a.pairs == a.head_dim ? ROT_PAIRS : ROT_SOME_PAIRS;
+                  : a.halves    ? (eights ? ROT_HALVES : ROT_ANY_HALVES)
+                                : (eights ? ROT_PAIRS : ROT_ANY_PAIRS);
   a.waves = 0;
   for (RopePart& p : a.part) {
     p.waves = 0;
@@ -251,7 +328,9 @@ hipError_t launch_rope(const RopeArgs& args, hipStream_t stream) {
     if (p.codes)
       while (p.unit_heads * a.head_dim % 32 != 0) ++p.unit_heads;
     p.lanes = p.unit_heads * pieces;
-    p.tokens = 64 / p.lanes;
+    // tokens of a wave: their rows lie within the 2^31 bytes of a buffer
+    const int64_t row_bytes = 2 * std::max(p.x_stride, p.codes ? 0 : p.out_stride);
+    p.tokens = (int)std::clamp<int64_t>((int64_t(1) << 30) / row_bytes, 1, 64 / p.lanes);
     p.units = (p.heads + p.unit_heads - 1) / p.unit_heads;
     const int64_t tiles = (a.tokens + p.tokens - 1) / p.tokens;
     // units of a wave: all of a token's, or fewer where that leaves the GPU idle
@@ -264,11 +343,10 @@ hipError_t launch_rope(const RopeArgs& args, hipStream_t stream) {
   }
   const int64_t most = int64_t(1) << 22, need = (a.waves + 3) / 4;
   const dim3 grid((unsigned)(need < most ? need : most));
-  static const void* const kernels[4][2] = {
-      {(const void*)&rope_kernel<ROT_NONE, false>, (const void*)&rope_kernel<ROT_NONE, true>},
-      {(const void*)&rope_kernel<ROT_PAIRS, false>, (const void*)&rope_kernel<ROT_PAIRS, true>},
-      {(const void*)&rope_kernel<ROT_SOME_PAIRS, false>, (const void*)&rope_kernel<ROT_SOME_PAIRS, true>},
-      {(const void*)&rope_kernel<ROT_HALVES, false>, (const void*)&rope_kernel<ROT_HALVES, true>}};
+#define KQ_ROPE(ROT) {(const void*)&rope_kernel<ROT, false>, (const void*)&rope_kernel<ROT, true>}
+  static const void* const kernels[5][2] = {KQ_ROPE(ROT_NONE), KQ_ROPE(ROT_PAIRS), KQ_ROPE(ROT_HALVES),
+                                            KQ_ROPE(ROT_ANY_PAIRS), KQ_ROPE(ROT_ANY_HALVES)};
+#undef KQ_ROPE
   void* kargs[] = {&a};
   return hipLaunchKernel(kernels[rot][a.norm], grid, dim3(kThreads), kargs, 0, stream);
 }
