@@ -234,6 +234,23 @@ def test_rows_past_4_gib():
     ref.check(x.contiguous(), *ref.rope(rows, heads, rotation))
 
 
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("dim,kv_heads", [(128, 3), (64, 5), (72, 4), (16, 2)])
+def test_keys_far_apart(dim, kv_heads, halves):
+    """Strides that no buffer spans over the tokens of a wave."""
+    W, tokens, stride = kv_heads * dim, 5, (1 << 29) + 8
+    flat = torch.zeros((tokens - 1) * stride + W, dtype=torch.bfloat16, device=DEV)
+    k = flat.as_strided((tokens, W), (stride, 1))
+    rows = cref.bf16((tokens, W), 4)
+    k.copy_(rows.to(DEV))
+    rotation = turn(tokens, (dim,), halves, 3)
+    pools = kq.alloc_cache(tokens, W, DEV)
+    slots = torch.arange(tokens, dtype=torch.int32, device=DEV)
+    kq.kq_cache_write_rope(k, None, slots, pools[0], pools[1], None, None, kv_heads, on_gpu(rotation), kq.KQ_NORM_RMS)
+    turned = ref.rounded(ref.rope(rows, kv_heads, rotation, True)[0]).to(torch.bfloat16)
+    ref.check_codes(pools[0], pools[1], turned)
+
+
 def test_more_heads_than_a_round_of_the_gpu():
     """Many tokens of small heads, and one token of many."""
     for tokens, heads, dim in ((70001, 1, 8), (1, 4099, 8), (2, 700, 72)):

@@ -166,9 +166,8 @@ struct RopePart {  // queries (or any rows), keys or values of a call; heads 0: 
   const float* weight;  // of the norm, [head_dim] (null: 1)
   int heads;
   bool turn;  // false: taken as they are (values)
-  // set by launch_rope: heads and lanes of a unit, tokens of a wave, units of a token, units of a wave, waves of a
-  // wave's tokens, waves in all
-  int unit_heads, lanes, tokens, units, per, chunks;
+  // set by launch_rope: tokens and heads of a wave, waves of a wave's tokens, waves in all
+  int tokens, per, chunks;
   int64_t waves;
 };
 
@@ -188,6 +187,7 @@ struct RopeArgs {
   int n_slots;
   // set by launch_rope
   int64_t waves;
+  Divisor by_value_chunks;  // pieces of a row of values
   double inv_dim;
 };
 

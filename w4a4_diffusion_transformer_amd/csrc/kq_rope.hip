@@ -12,15 +12,17 @@
 //
 // Layout.  A lane holds 8 channels of a head: four whole pairs, that is one
 // 16-byte piece where pairs are neighbours, two of 8 bytes, R/2 apart, where
-// they are halves, and the piece of its own where they do not turn.  A unit is
-// the fewest heads whose pieces are whole blocks of 32 (one head for rows that
-// are not quantized); a wave takes as many tokens as units fit its 64 lanes
-// and goes over the units of those tokens, so a lane's channels and position
-// never change and its cosines and sines, with the weights, are formed once.
-// Halves are brought back into pieces through the wave's own LDS before they
-// are quantized.  R that is no multiple of 8 takes a slower form: a lane holds
-// a piece and fetches each partner.
+// they are halves, and the piece of its own where they do not turn.  A wave
+// takes as many tokens as heads fit its 64 lanes and goes over the heads of
+// those tokens, four at a time, so a lane's channels and position never change
+// and its cosines and sines, with the weights, are formed once.  Keys then go
+// through the wave's own LDS, four heads of its tokens as one run of pieces:
+// blocks of 32 channels that span heads come out in four adjacent lanes, as
+// kq_cache_write's do.  Values are taken as that call takes them.  R that is no
+// multiple of 8 takes a slower form: a lane holds a piece and fetches each
+// partner.
 #include <algorithm>
+#include <type_traits>
 
 #include "kq_device.hpp"
 #include "kq_internal.h"
@@ -32,7 +34,7 @@ namespace kq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // units whose loads a lane has in flight
+constexpr int kBatch = 4;  // heads (pieces of values) that a lane has in flight
 
 // How pairs lie: not at all; neighbours or halves with R a multiple of 8; either with any R.
 enum { ROT_NONE = 0, ROT_PAIRS = 1, ROT_HALVES = 2, ROT_ANY_PAIRS = 3, ROT_ANY_HALVES = 4 };
@@ -162,7 +164,7 @@ struct AnyPairs {
   int from[8];  // the partner's channel, or the channel itself
   bool turns[8];
 
-  __device__ __forceinline__ void form(const RopeArgs& a, int64_t row, const float* weight, int c) {
+  __device__ __forceinline__ void form(const RopeArgs& a, int64_t row, const float* weight, int c, int, int) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int ch = 8 * c + j;
@@ -186,14 +188,48 @@ struct AnyPairs {
   }
 };
 
+// Codes and scale of a piece at place `chunk` of slot `slot`; the piece's block lies in four adjacent lanes.
+__device__ __forceinline__ void store_piece(const RopeArgs& a, const RopePart& s, u32x4 v, int slot, int chunk) {
+  unsigned word, byte;
+  quantize_piece(v, word, byte);
+  if ((unsigned)slot < (unsigned)a.n_slots) {  // a token without a slot writes nothing
+    const int chunks = s.heads * (a.head_dim >> 3);
+    *reinterpret_cast<unsigned*>(s.codes + (int64_t)slot * (4 * chunks) + 4 * chunk) = word;
+    if ((chunk & 3) == 0) s.scales[(int64_t)slot * (chunks >> 2) + (chunk >> 2)] = (uint8_t)byte;
+  }
+}
+
+// Values: kBatch * 64 consecutive pieces of the rows.
+__device__ __forceinline__ void write_values(const RopeArgs& a, const RopePart& s, int64_t index, int lane) {
+  const int chunks = s.heads * (a.head_dim >> 3);
+  const int64_t base = index * (64 * kBatch);
+  const int64_t row0 = base / chunks;
+  const unsigned first = (unsigned)(base - row0 * chunks) + lane;
+  u32x4 in[kBatch];
+  int slot[kBatch], chunk[kBatch];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const unsigned at = first + 64 * k, r = fast_div(at, a.by_value_chunks);
+    const int64_t row = row0 + r;
+    chunk[k] = (int)(at - r * (unsigned)chunks);
+    in[k] = u32x4{0, 0, 0, 0};
+    slot[k] = -1;
+    if (row < a.tokens) {
+      in[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(s.x + row * s.x_stride + 8 * chunk[k]));
+      slot[k] = a.slots[row];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) store_piece(a, s, in[k], slot[k], chunk[k]);
+}
+
 template <int ROT, bool NORM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   constexpr bool kAny = ROT >= ROT_ANY_PAIRS;
-  constexpr bool kStage = kAny || ROT == ROT_HALVES;
-  __shared__ u32x4 stage[kStage ? kThreads : 1];
+  __shared__ u32x4 stage[kThreads * kBatch];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  u32x4* const mine = stage + (kStage ? 64 * wave : 0);
+  u32x4* const mine = stage + 64 * kBatch * wave;
   const int pieces = a.head_dim >> 3;
   for (int64_t index = (int64_t)blockIdx.x * (kThreads / 64) + wave; index < a.waves;
        index += (int64_t)gridDim.x * (kThreads / 64)) {
@@ -201,110 +237,105 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     int which = 0;
     while (i >= a.part[which].waves) i -= a.part[which++].waves;
     const RopePart& s = a.part[which];
+    if (!s.turn) {
+      write_values(a, s, i, lane);
+      continue;
+    }
     const int64_t tile = i / s.chunks;
-    const int unit0 = (int)(i - tile * s.chunks) * s.per;
-    const int unit1 = unit0 + s.per < s.units ? unit0 + s.per : s.units;
-    // this lane's token, head within a unit and place within the head
-    const int of_token = lane / s.lanes;
-    const bool used = of_token < s.tokens;  // lanes past the last whole unit do as lane 0
-    const int in_unit = used ? lane - of_token * s.lanes : 0;
-    const int of_head = in_unit / pieces, c = in_unit - of_head * pieces;
-    const int first = used ? lane - c : 0;  // the head's first lane
-    const int64_t t0 = tile * s.tokens, t = t0 + (used ? of_token : 0);
-    bool live = used && t < a.tokens;
+    const int head0 = (int)(i - tile * s.chunks) * s.per;
+    const int head1 = head0 + s.per < s.heads ? head0 + s.per : s.heads;
+    // this lane's token and place within a head
+    const int of_token = lane / pieces;
+    const bool used = of_token < s.tokens;  // lanes past the last whole head do as lane 0
+    const int token = used ? of_token : 0, c = used ? lane - token * pieces : 0;
+    const int first = token * pieces;  // the head's first lane
+    const int64_t t0 = tile * s.tokens, t = t0 + token;
+    const bool live = used && t < a.tokens;
     const int64_t row = t < a.tokens ? t : a.tokens - 1;
     const bool cache = s.codes != nullptr;
     // channels of the first and the last four values
-    const bool apart = ROT == ROT_HALVES && s.turn && 4 * c < a.pairs;
+    const bool apart = ROT == ROT_HALVES && 4 * c < a.pairs;
     const int lo = apart ? 4 * c : 8 * c, hi = apart ? a.pairs + 4 * c : 8 * c + 4;
 
     // the rows of the wave's tokens are one buffer; heads are added as a scalar offset
     const int64_t rows = t0 + s.tokens < a.tokens ? s.tokens : a.tokens - t0;
     const auto rx = rsrc_uniform(s.x + t0 * s.x_stride, 2 * ((rows - 1) * s.x_stride + (int64_t)s.heads * a.head_dim));
-    const int of_row = 2 * ((int)(row - t0) * (int)s.x_stride + of_head * a.head_dim);
+    const int of_row = 2 * (int)(row - t0) * (int)s.x_stride;
     const int at_lo = of_row + 2 * lo, at_hi = of_row + 2 * hi;
-    auto load = [&](int unit) {
-      const int head = (unit < unit1 ? unit : unit1 - 1) * s.unit_heads * a.head_dim * 2;
+    auto load = [&](int head) {
+      const int at = (head < head1 ? head : head1 - 1) * a.head_dim * 2;
       if constexpr (ROT == ROT_HALVES) {
-        const u32x2 l = __builtin_amdgcn_raw_buffer_load_b64(rx, at_lo, head, 0);
-        const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(rx, at_hi, head, 0);
+        const u32x2 l = __builtin_amdgcn_raw_buffer_load_b64(rx, at_lo, at, 0);
+        const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(rx, at_hi, at, 0);
         return u32x4{l[0], l[1], h[0], h[1]};
       } else {
-        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at_lo, head, 0));
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at_lo, at, 0));
       }
     };
     u32x4 in[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) in[k] = load(unit0 + k);
+    for (int k = 0; k < kBatch; ++k) in[k] = load(head0 + k);
+    const int slot = cache && live ? a.slots[row] : -1;
 
-    int64_t slot = 0;
-    if (cache) {
-      const int at = a.slots[row];
-      live = live && (unsigned)at < (unsigned)a.n_slots;  // a token without a slot writes nothing
-      slot = live ? at : 0;
-    }
-    WholePairs<ROT> whole;
-    AnyPairs<ROT> any;
-    if (s.turn) {
-      const float* const weight = NORM ? s.weight : nullptr;
-      if constexpr (kAny) any.form(a, row, weight, c);
-      else whole.form(a, row, weight, c, lo, hi);
-    }
-    uint8_t* const codes = s.codes + slot * (s.heads * pieces * 4) + 4 * in_unit;
-    uint8_t* const scales = s.scales + slot * (s.heads * pieces >> 2) + (in_unit >> 2);
+    std::conditional_t<kAny, AnyPairs<ROT>, WholePairs<ROT>> turns;
+    turns.form(a, row, NORM ? s.weight : nullptr, c, lo, hi);
     const auto ro = rsrc_uniform(s.out + t0 * s.out_stride, 2 * ((rows - 1) * s.out_stride + (int64_t)s.heads * a.head_dim));
-    const int of_out = 2 * ((int)(row - t0) * (int)s.out_stride + of_head * a.head_dim);
+    const int of_out = 2 * (int)(row - t0) * (int)s.out_stride;
     const int out_lo = live ? of_out + 2 * lo : (int)kOut, out_hi = live ? of_out + 2 * hi : (int)kOut;
 
-    for (int u0 = unit0; u0 < unit1; u0 += kBatch) {
-      if (u0 > unit0) {
+    for (int h0 = head0; h0 < head1; h0 += kBatch) {
+      const int heads = head1 - h0 < kBatch ? head1 - h0 : kBatch;
+      if (h0 > head0) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) in[k] = load(u0 + k);
+        for (int k = 0; k < kBatch; ++k) in[k] = load(h0 + k);
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (u0 + k >= unit1) break;  // uniform
+        if (k >= heads) break;  // uniform
         u32x4 v = in[k];
-        if (s.turn) {
-          double y[8];
-          piece_values(v, y);
-          double r = 1.0;
-          if constexpr (NORM) r = head_scale(a, y, pieces, first, c);
-          if constexpr (kAny) {
-            mine[lane] = v;
-            wave_lds_fence();
-            any.apply(y, r, reinterpret_cast<const uint16_t*>(mine + first));
-            wave_lds_fence();
-          } else {
-            whole.apply(y, r);
-          }
-          v = round_piece(y);
+        double y[8];
+        piece_values(v, y);
+        double r = 1.0;
+        if constexpr (NORM) r = head_scale(a, y, pieces, first, c);
+        u32x4* const head = mine + (token * heads + k) * pieces;  // a run of heads for each token
+        if constexpr (kAny) {
+          if (used) head[c] = v;
+          wave_lds_fence();
+          turns.apply(y, r, reinterpret_cast<const uint16_t*>(head));
+          wave_lds_fence();
+        } else {
+          turns.apply(y, r);
         }
-        const int unit = u0 + k;
+        v = round_piece(y);
         if (cache) {
-          if (ROT == ROT_HALVES && s.turn) {  // back into pieces
-            u32x2* const head = reinterpret_cast<u32x2*>(mine + first);
-            head[lo >> 2] = u32x2{v[0], v[1]};
-            head[hi >> 2] = u32x2{v[2], v[3]};
-            wave_lds_fence();
-            v = mine[lane];
-            wave_lds_fence();
-          }
-          unsigned word, byte;
-          quantize_piece(v, word, byte);
-          if (live) {
-            *reinterpret_cast<unsigned*>(codes + 4 * unit * s.lanes) = word;
-            if ((in_unit & 3) == 0) scales[unit * s.lanes >> 2] = (uint8_t)byte;
+          u32x2* const fours = reinterpret_cast<u32x2*>(head);
+          if (used) {
+            fours[lo >> 2] = u32x2{v[0], v[1]};
+            fours[hi >> 2] = u32x2{v[2], v[3]};
           }
         } else {
-          const int head = unit * s.unit_heads * a.head_dim * 2;
+          const int at = (h0 + k) * a.head_dim * 2;
           if constexpr (ROT == ROT_HALVES) {
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, out_lo, head, 0);
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[2], v[3]}, ro, out_hi, head, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, out_lo, at, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[2], v[3]}, ro, out_hi, at, 0);
           } else {
-            __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_lo, head, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_lo, at, 0);
           }
         }
+      }
+      if (cache) {
+        wave_lds_fence();
+        const int run = heads * pieces;                     // pieces of a token, whole blocks of 32
+        const unsigned by_run = 65536u / (unsigned)run + 1u;  // n / run for n < 256: n by_run >> 16
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int n = 64 * k + lane;
+          const int tk = (int)((unsigned)n * by_run >> 16);
+          const int at = __builtin_amdgcn_ds_bpermute(4 * tk * pieces, slot);
+          const bool there = tk < s.tokens;
+          store_piece(a, s, mine[n], there ? at : -1, h0 * pieces + n - tk * run);
+        }
+        wave_lds_fence();
       }
     }
   }
@@ -324,20 +355,24 @@ hipError_t launch_rope(const RopeArgs& args, hipStream_t stream) {
   for (RopePart& p : a.part) {
     p.waves = 0;
     if (p.heads == 0) continue;
-    p.unit_heads = 1;
-    if (p.codes)
-      while (p.unit_heads * a.head_dim % 32 != 0) ++p.unit_heads;
-    p.lanes = p.unit_heads * pieces;
+    if (!p.turn) {
+      a.by_value_chunks = make_divisor((unsigned)(p.heads * pieces));
+      p.waves = (a.tokens * p.heads * pieces + 64 * kBatch - 1) / (64 * kBatch);
+      a.waves += p.waves;
+      continue;
+    }
     // tokens of a wave: their rows lie within the 2^31 bytes of a buffer
     const int64_t row_bytes = 2 * std::max(p.x_stride, p.codes ? 0 : p.out_stride);
-    p.tokens = (int)std::clamp<int64_t>((int64_t(1) << 30) / row_bytes, 1, 64 / p.lanes);
-    p.units = (p.heads + p.unit_heads - 1) / p.unit_heads;
+    p.tokens = (int)std::clamp<int64_t>((int64_t(1) << 30) / row_bytes, 1, 64 / pieces);
     const int64_t tiles = (a.tokens + p.tokens - 1) / p.tokens;
-    // units of a wave: all of a token's, or fewer where that leaves the GPU idle
-    int64_t chunks = (int64_t)cu_count() * 8 / tiles;
-    chunks = chunks < 1 ? 1 : chunks > p.units ? p.units : chunks;
-    p.per = (int)((p.units + chunks - 1) / chunks);
-    p.chunks = (p.units + p.per - 1) / p.per;
+    // heads of a wave: all of its tokens', or fewer (but whole blocks of 32) where that leaves the GPU idle
+    int unit = 1;
+    while (p.codes && unit * a.head_dim % 32 != 0) ++unit;
+    const int64_t units = (p.heads + unit - 1) / unit;
+    const int64_t chunks = std::clamp<int64_t>((8 * (int64_t)cu_count() + tiles - 1) / tiles, 1, units);
+    p.per = (int)((units + chunks - 1) / chunks) * unit;
+    if (p.per > kBatch) p.per = (p.per + kBatch - 1) / kBatch * kBatch;
+    p.chunks = (p.heads + p.per - 1) / p.per;
     p.waves = tiles * p.chunks;
     a.waves += p.waves;
   }
