@@ -186,7 +186,7 @@ struct RopeArgs {
   const int32_t* slots;
   int n_slots;
   // set by launch_rope
-  int64_t waves;
+  int64_t waves, first_wave;
   Divisor by_value_chunks;  // pieces of a row of values
   double inv_dim;
 };

@@ -231,112 +231,111 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   u32x4* const mine = stage + 64 * kBatch * wave;
   const int pieces = a.head_dim >> 3;
-  for (int64_t index = (int64_t)blockIdx.x * (kThreads / 64) + wave; index < a.waves;
-       index += (int64_t)gridDim.x * (kThreads / 64)) {
-    int64_t i = index;
-    int which = 0;
-    while (i >= a.part[which].waves) i -= a.part[which++].waves;
-    const RopePart& s = a.part[which];
-    if (!s.turn) {
-      write_values(a, s, i, lane);
-      continue;
+  int64_t i = a.first_wave + (int64_t)blockIdx.x * (kThreads / 64) + wave;
+  if (i >= a.waves) return;
+  int which = 0;
+  while (i >= a.part[which].waves) i -= a.part[which++].waves;
+  const RopePart& s = a.part[which];
+  if (!s.turn) {
+    write_values(a, s, i, lane);
+    return;
+  }
+  const int64_t tile = i / s.chunks;
+  const int head0 = (int)(i - tile * s.chunks) * s.per;
+  const int head1 = head0 + s.per < s.heads ? head0 + s.per : s.heads;
+  // this lane's token and place within a head
+  const int of_token = lane / pieces;
+  const bool used = of_token < s.tokens;  // lanes past the last whole head do as lane 0
+  const int token = used ? of_token : 0, c = used ? lane - token * pieces : 0;
+  const int first = token * pieces;  // the head's first lane
+  const int64_t t0 = tile * s.tokens, t = t0 + token;
+  const bool live = used && t < a.tokens;
+  const int64_t row = t < a.tokens ? t : a.tokens - 1;
+  const bool cache = s.codes != nullptr;
+  // channels of the first and the last four values
+  const bool apart = ROT == ROT_HALVES && 4 * c < a.pairs;
+  const int lo = apart ? 4 * c : 8 * c, hi = apart ? a.pairs + 4 * c : 8 * c + 4;
+
+  // the rows of the wave's tokens are one buffer; heads are added as a scalar offset
+  const int64_t rows = t0 + s.tokens < a.tokens ? s.tokens : a.tokens - t0;
+  const auto rx = rsrc_uniform(s.x + t0 * s.x_stride, 2 * ((rows - 1) * s.x_stride + (int64_t)s.heads * a.head_dim));
+  const int of_row = 2 * (int)(row - t0) * (int)s.x_stride;
+  const int at_lo = of_row + 2 * lo, at_hi = of_row + 2 * hi;
+  auto load = [&](int head) {
+    const int at = (head < head1 ? head : head1 - 1) * a.head_dim * 2;
+    if constexpr (ROT == ROT_HALVES) {
+      const u32x2 l = __builtin_amdgcn_raw_buffer_load_b64(rx, at_lo, at, 0);
+      const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(rx, at_hi, at, 0);
+      return u32x4{l[0], l[1], h[0], h[1]};
+    } else {
+      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at_lo, at, 0));
     }
-    const int64_t tile = i / s.chunks;
-    const int head0 = (int)(i - tile * s.chunks) * s.per;
-    const int head1 = head0 + s.per < s.heads ? head0 + s.per : s.heads;
-    // this lane's token and place within a head
-    const int of_token = lane / pieces;
-    const bool used = of_token < s.tokens;  // lanes past the last whole head do as lane 0
-    const int token = used ? of_token : 0, c = used ? lane - token * pieces : 0;
-    const int first = token * pieces;  // the head's first lane
-    const int64_t t0 = tile * s.tokens, t = t0 + token;
-    const bool live = used && t < a.tokens;
-    const int64_t row = t < a.tokens ? t : a.tokens - 1;
-    const bool cache = s.codes != nullptr;
-    // channels of the first and the last four values
-    const bool apart = ROT == ROT_HALVES && 4 * c < a.pairs;
-    const int lo = apart ? 4 * c : 8 * c, hi = apart ? a.pairs + 4 * c : 8 * c + 4;
+  };
+  u32x4 in[kBatch];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) in[k] = load(head0 + k);
+  const int slot = cache && live ? a.slots[row] : -1;
 
-    // the rows of the wave's tokens are one buffer; heads are added as a scalar offset
-    const int64_t rows = t0 + s.tokens < a.tokens ? s.tokens : a.tokens - t0;
-    const auto rx = rsrc_uniform(s.x + t0 * s.x_stride, 2 * ((rows - 1) * s.x_stride + (int64_t)s.heads * a.head_dim));
-    const int of_row = 2 * (int)(row - t0) * (int)s.x_stride;
-    const int at_lo = of_row + 2 * lo, at_hi = of_row + 2 * hi;
-    auto load = [&](int head) {
-      const int at = (head < head1 ? head : head1 - 1) * a.head_dim * 2;
-      if constexpr (ROT == ROT_HALVES) {
-        const u32x2 l = __builtin_amdgcn_raw_buffer_load_b64(rx, at_lo, at, 0);
-        const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(rx, at_hi, at, 0);
-        return u32x4{l[0], l[1], h[0], h[1]};
+  std::conditional_t<kAny, AnyPairs<ROT>, WholePairs<ROT>> turns;
+  turns.form(a, row, NORM ? s.weight : nullptr, c, lo, hi);
+  const auto ro = rsrc_uniform(s.out + t0 * s.out_stride, 2 * ((rows - 1) * s.out_stride + (int64_t)s.heads * a.head_dim));
+  const int of_out = 2 * (int)(row - t0) * (int)s.out_stride;
+  const int out_lo = live ? of_out + 2 * lo : (int)kOut, out_hi = live ? of_out + 2 * hi : (int)kOut;
+
+  for (int h0 = head0; h0 < head1; h0 += kBatch) {
+    const int heads = head1 - h0 < kBatch ? head1 - h0 : kBatch;
+    if (h0 > head0) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) in[k] = load(h0 + k);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (k >= heads) break;  // uniform
+      u32x4 v = in[k];
+      double y[8];
+      piece_values(v, y);
+      double r = 1.0;
+      if constexpr (NORM) r = head_scale(a, y, pieces, first, c);
+      u32x4* const head = mine + (token * heads + k) * pieces;  // a run of heads for each token
+      if constexpr (kAny) {
+        if (used) head[c] = v;
+        wave_lds_fence();
+        turns.apply(y, r, reinterpret_cast<const uint16_t*>(head));
+        wave_lds_fence();
       } else {
-        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at_lo, at, 0));
+        turns.apply(y, r);
       }
-    };
-    u32x4 in[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) in[k] = load(head0 + k);
-    const int slot = cache && live ? a.slots[row] : -1;
-
-    std::conditional_t<kAny, AnyPairs<ROT>, WholePairs<ROT>> turns;
-    turns.form(a, row, NORM ? s.weight : nullptr, c, lo, hi);
-    const auto ro = rsrc_uniform(s.out + t0 * s.out_stride, 2 * ((rows - 1) * s.out_stride + (int64_t)s.heads * a.head_dim));
-    const int of_out = 2 * (int)(row - t0) * (int)s.out_stride;
-    const int out_lo = live ? of_out + 2 * lo : (int)kOut, out_hi = live ? of_out + 2 * hi : (int)kOut;
-
-    for (int h0 = head0; h0 < head1; h0 += kBatch) {
-      const int heads = head1 - h0 < kBatch ? head1 - h0 : kBatch;
-      if (h0 > head0) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) in[k] = load(h0 + k);
+      v = round_piece(y);
+      if (cache) {
+        u32x2* const fours = reinterpret_cast<u32x2*>(head);
+        if (used) {
+          fours[lo >> 2] = u32x2{v[0], v[1]};
+          fours[hi >> 2] = u32x2{v[2], v[3]};
+        }
+      } else {
+        const int at = (h0 + k) * a.head_dim * 2;
+        if constexpr (ROT == ROT_HALVES) {
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, out_lo, at, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[2], v[3]}, ro, out_hi, at, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_lo, at, 0);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);  // one head at a time: registers for a fifth wave
+    }
+    if (cache) {
+      wave_lds_fence();
+      const int run = heads * pieces;                     // pieces of a token, whole blocks of 32
+      const unsigned by_run = 65536u / (unsigned)run + 1u;  // n / run for n < 256: n by_run >> 16
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (k >= heads) break;  // uniform
-        u32x4 v = in[k];
-        double y[8];
-        piece_values(v, y);
-        double r = 1.0;
-        if constexpr (NORM) r = head_scale(a, y, pieces, first, c);
-        u32x4* const head = mine + (token * heads + k) * pieces;  // a run of heads for each token
-        if constexpr (kAny) {
-          if (used) head[c] = v;
-          wave_lds_fence();
-          turns.apply(y, r, reinterpret_cast<const uint16_t*>(head));
-          wave_lds_fence();
-        } else {
-          turns.apply(y, r);
-        }
-        v = round_piece(y);
-        if (cache) {
-          u32x2* const fours = reinterpret_cast<u32x2*>(head);
-          if (used) {
-            fours[lo >> 2] = u32x2{v[0], v[1]};
-            fours[hi >> 2] = u32x2{v[2], v[3]};
-          }
-        } else {
-          const int at = (h0 + k) * a.head_dim * 2;
-          if constexpr (ROT == ROT_HALVES) {
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, out_lo, at, 0);
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[2], v[3]}, ro, out_hi, at, 0);
-          } else {
-            __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_lo, at, 0);
-          }
-        }
+        const int n = 64 * k + lane;
+        const int tk = (int)((unsigned)n * by_run >> 16);
+        const int at = __builtin_amdgcn_ds_bpermute(4 * tk * pieces, slot);
+        const bool there = tk < s.tokens;
+        store_piece(a, s, mine[n], there ? at : -1, h0 * pieces + n - tk * run);
       }
-      if (cache) {
-        wave_lds_fence();
-        const int run = heads * pieces;                     // pieces of a token, whole blocks of 32
-        const unsigned by_run = 65536u / (unsigned)run + 1u;  // n / run for n < 256: n by_run >> 16
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int n = 64 * k + lane;
-          const int tk = (int)((unsigned)n * by_run >> 16);
-          const int at = __builtin_amdgcn_ds_bpermute(4 * tk * pieces, slot);
-          const bool there = tk < s.tokens;
-          store_piece(a, s, mine[n], there ? at : -1, h0 * pieces + n - tk * run);
-        }
-        wave_lds_fence();
-      }
+      wave_lds_fence();
     }
   }
 }
@@ -376,14 +375,19 @@ hipError_t launch_rope(const RopeArgs& args, hipStream_t stream) {
     p.waves = tiles * p.chunks;
     a.waves += p.waves;
   }
-  const int64_t most = int64_t(1) << 22, need = (a.waves + 3) / 4;
-  const dim3 grid((unsigned)(need < most ? need : most));
 #define KQ_ROPE(ROT) {(const void*)&rope_kernel<ROT, false>, (const void*)&rope_kernel<ROT, true>}
   static const void* const kernels[5][2] = {KQ_ROPE(ROT_NONE), KQ_ROPE(ROT_PAIRS), KQ_ROPE(ROT_HALVES),
                                             KQ_ROPE(ROT_ANY_PAIRS), KQ_ROPE(ROT_ANY_HALVES)};
 #undef KQ_ROPE
-  void* kargs[] = {&a};
-  return hipLaunchKernel(kernels[rot][a.norm], grid, dim3(kThreads), kargs, 0, stream);
+  const int64_t most = int64_t(1) << 23;  // workgroups of a launch, which has less than 2^32 threads
+  for (a.first_wave = 0; a.first_wave < a.waves; a.first_wave += most * (kThreads / 64)) {
+    const int64_t need = (a.waves - a.first_wave + kThreads / 64 - 1) / (kThreads / 64);
+    void* kargs[] = {&a};
+    const hipError_t e = hipLaunchKernel(kernels[rot][a.norm], dim3((unsigned)std::min(need, most)), dim3(kThreads), kargs,
+                                         0, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace kq
