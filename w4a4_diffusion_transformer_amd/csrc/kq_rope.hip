@@ -261,14 +261,17 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   const auto rx = rsrc_uniform(s.x + t0 * s.x_stride, 2 * ((rows - 1) * s.x_stride + (int64_t)s.heads * a.head_dim));
   const int of_row = 2 * (int)(row - t0) * (int)s.x_stride;
   const int at_lo = of_row + 2 * lo, at_hi = of_row + 2 * hi;
+  constexpr int kPast = (int)0x80000000u;  // it and what a head adds lie past every buffer: nothing is read or written
   auto load = [&](int head) {
-    const int at = (head < head1 ? head : head1 - 1) * a.head_dim * 2;
+    const int at = head * a.head_dim * 2;
+    const bool there = head < head1;  // uniform
     if constexpr (ROT == ROT_HALVES) {
-      const u32x2 l = __builtin_amdgcn_raw_buffer_load_b64(rx, at_lo, at, 0);
-      const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(rx, at_hi, at, 0);
+      const u32x2 l = __builtin_amdgcn_raw_buffer_load_b64(rx, there ? at_lo : kPast, there ? at : 0, 0);
+      const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(rx, there ? at_hi : kPast, there ? at : 0, 0);
       return u32x4{l[0], l[1], h[0], h[1]};
     } else {
-      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at_lo, at, 0));
+      return __builtin_bit_cast(u32x4,
+                                __builtin_amdgcn_raw_buffer_load_b128(rx, there ? at_lo : kPast, there ? at : 0, 0));
     }
   };
   u32x4 in[kBatch];
@@ -280,64 +283,80 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   turns.form(a, row, NORM ? s.weight : nullptr, c, lo, hi);
   const auto ro = rsrc_uniform(s.out + t0 * s.out_stride, 2 * ((rows - 1) * s.out_stride + (int64_t)s.heads * a.head_dim));
   const int of_out = 2 * (int)(row - t0) * (int)s.out_stride;
-  const int out_lo = live ? of_out + 2 * lo : (int)kOut, out_hi = live ? of_out + 2 * hi : (int)kOut;
+  const int out_lo = live ? of_out + 2 * lo : kPast, out_hi = live ? of_out + 2 * hi : kPast;
 
-  for (int h0 = head0; h0 < head1; h0 += kBatch) {
-    const int heads = head1 - h0 < kBatch ? head1 - h0 : kBatch;
-    if (h0 > head0) {
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) in[k] = load(h0 + k);
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (k >= heads) break;  // uniform
-      u32x4 v = in[k];
-      double y[8];
-      piece_values(v, y);
-      double r = 1.0;
-      if constexpr (NORM) r = head_scale(a, y, pieces, first, c);
-      u32x4* const head = mine + (token * heads + k) * pieces;  // a run of heads for each token
-      if constexpr (kAny) {
-        if (used) head[c] = v;
-        wave_lds_fence();
-        turns.apply(y, r, reinterpret_cast<const uint16_t*>(head));
-        wave_lds_fence();
-      } else {
-        turns.apply(y, r);
-      }
-      v = round_piece(y);
-      if (cache) {
-        u32x2* const fours = reinterpret_cast<u32x2*>(head);
-        if (used) {
-          fours[lo >> 2] = u32x2{v[0], v[1]};
-          fours[hi >> 2] = u32x2{v[2], v[3]};
-        }
-      } else {
-        const int at = (h0 + k) * a.head_dim * 2;
-        if constexpr (ROT == ROT_HALVES) {
-          __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, out_lo, at, 0);
-          __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[2], v[3]}, ro, out_hi, at, 0);
-        } else {
-          __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_lo, at, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);  // one head at a time: registers for a fifth wave
-    }
-    if (cache) {
+  // Head k of the batch of `heads` from h0 on.  As soon as a head's values are out of their registers, those of the
+  // head kBatch further on are on their way into them.  Keys and rows have loops of their own, and whole batches one
+  // without a condition, so that how many stores lie behind a load is known when compiling, and with it the wait.
+  auto turn_head = [&](auto keys, int h0, int heads, int k) {
+    u32x4 v = in[k];
+    double y[8];
+    piece_values(v, y);
+    in[k] = load(h0 + kBatch + k);
+    double r = 1.0;
+    if constexpr (NORM) r = head_scale(a, y, pieces, first, c);
+    u32x4* const head = mine + (token * heads + k) * pieces;  // a run of heads for each token
+    if constexpr (kAny) {
+      if (used) head[c] = v;
       wave_lds_fence();
-      const int run = heads * pieces;                     // pieces of a token, whole blocks of 32
-      const unsigned by_run = 65536u / (unsigned)run + 1u;  // n / run for n < 256: n by_run >> 16
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int n = 64 * k + lane;
-        const int tk = (int)((unsigned)n * by_run >> 16);
-        const int at = __builtin_amdgcn_ds_bpermute(4 * tk * pieces, slot);
-        const bool there = tk < s.tokens;
-        store_piece(a, s, mine[n], there ? at : -1, h0 * pieces + n - tk * run);
-      }
+      turns.apply(y, r, reinterpret_cast<const uint16_t*>(head));
       wave_lds_fence();
+    } else {
+      turns.apply(y, r);
     }
-  }
+    v = round_piece(y);
+    if constexpr (decltype(keys)::value) {
+      u32x2* const fours = reinterpret_cast<u32x2*>(head);
+      if (used) {
+        fours[lo >> 2] = u32x2{v[0], v[1]};
+        fours[hi >> 2] = u32x2{v[2], v[3]};
+      }
+    } else {
+      // The head is added to the lane's offset, not given as the instruction's scalar one: a 16-byte store with a
+      // scalar register for an offset reads its last lanes' data so late that the next instruction may have replaced
+      // it (seen as zeros in four lanes of 16), and the compiler puts the wait only behind stores without one.
+      const int at = (h0 + k) * a.head_dim * 2;
+      if constexpr (ROT == ROT_HALVES) {
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, ro, out_lo + at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[2], v[3]}, ro, out_hi + at, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_buffer_store_b128(v, ro, out_lo + at, 0, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto batches = [&](auto keys) {
+    auto write_keys = [&](int h0, int heads) {
+      if constexpr (decltype(keys)::value) {
+        wave_lds_fence();
+        const int run = heads * pieces;                       // pieces of a token, whole blocks of 32
+        const unsigned by_run = 65536u / (unsigned)run + 1u;  // n / run for n < 256: n by_run >> 16
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int n = 64 * k + lane;
+          const int tk = (int)((unsigned)n * by_run >> 16);
+          const int at = __builtin_amdgcn_ds_bpermute(4 * tk * pieces, slot);
+          store_piece(a, s, mine[n], tk < s.tokens ? at : -1, h0 * pieces + n - tk * run);
+        }
+        wave_lds_fence();
+      }
+    };
+    int h0 = head0;
+    for (; h0 + kBatch <= head1; h0 += kBatch) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) turn_head(keys, h0, kBatch, k);
+      write_keys(h0, kBatch);
+    }
+    const int heads = head1 - h0;
+    if (heads > 0) {
+#pragma unroll
+      for (int k = 0; k < kBatch - 1; ++k)
+        if (k < heads) turn_head(keys, h0, heads, k);
+      write_keys(h0, heads);
+    }
+  };
+  if (cache) batches(std::true_type{});
+  else batches(std::false_type{});
 }
 
 }  // namespace
