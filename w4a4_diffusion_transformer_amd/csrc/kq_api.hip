@@ -425,8 +425,8 @@ kq_status run_rope(const Rows& q, int64_t q_heads, const float* q_weight, const 
   a.norm = norm == KQ_NORM_RMS;
   a.eps = (double)eps;
   a.n_axes = axes;
-  for (int i = 0, end = 0; i < axes; ++i) a.axis_end[i] = end += rotation->axis_dims[i] / 2;
   a.pairs = (int)(turned / 2);
+  for (int i = 0, end = 0; i < 4; ++i) a.axis_end[i] = i + 1 < axes ? end += rotation->axis_dims[i] / 2 : a.pairs;
   if (axes > 0) {
     a.positions = rotation->positions;
     a.freqs = rotation->freqs;

@@ -180,7 +180,7 @@ struct RopeArgs {
   const int32_t* positions;  // [tokens][n_axes]
   const double* freqs;       // [pairs]
   int n_axes;                // 0: nothing turns
-  int axis_end[4];           // the pair after an axis' last
+  int axis_end[4];           // the pair after an axis' last; `pairs` for the last axis and past it
   int pairs;
   bool halves;
   const int32_t* slots;

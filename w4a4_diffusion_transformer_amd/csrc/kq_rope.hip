@@ -99,12 +99,21 @@ __device__ __forceinline__ double head_sum(double v, int pieces, int first, int 
   return total;
 }
 
-// The sine and cosine of pair p at a token.
-__device__ __forceinline__ void turn_of(const RopeArgs& a, int64_t row, int p, double& sn, double& cs) {
-  int axis = 0;
-  for (int k = 0; k < a.n_axes - 1; ++k) axis += p >= a.axis_end[k];
-  sincos_quarters((double)a.positions[row * a.n_axes + axis] * (a.freqs[p] * 0.63661977236758134308), sn, cs);  // 2 / pi
-}
+// Position and frequency of pair p at a token; all loads of a lane's pairs go out before the first is used.
+struct Angle {
+  int position;
+  double freq;
+  __device__ __forceinline__ void load(const RopeArgs& a, int64_t row, int p) {
+    int axis = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) axis += p >= a.axis_end[k];  // of axes that are not there, past every pair
+    position = a.positions[row * a.n_axes + axis];
+    freq = a.freqs[p];
+  }
+  __device__ __forceinline__ void turn(double& sn, double& cs) const {
+    sincos_quarters((double)position * (freq * 0.63661977236758134308), sn, cs);  // 2 / pi
+  }
+};
 
 // 1 / rms of the head that this lane's values are of.
 __device__ __forceinline__ double head_scale(const RopeArgs& a, const double y[8], int pieces, int first, int c) {
@@ -127,19 +136,29 @@ struct WholePairs {
   // lo, hi: the channels of the lane's first and last four values
   __device__ __forceinline__ void form(const RopeArgs& a, int64_t row, const float* weight, int c, int lo, int hi) {
     turns = ROT != ROT_NONE && 4 * c < a.pairs;
+    Angle angle[4];
+    float wu[4], wv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (ROT != ROT_NONE) angle[j].load(a, row, turns ? 4 * c + j : 0);
+      wu[j] = wv[j] = 1.0f;
+      if (weight) {  // uniform
+        wu[j] = weight[first_of(j) < 4 ? lo + first_of(j) : hi + first_of(j) - 4];
+        wv[j] = weight[second_of(j) < 4 ? lo + second_of(j) : hi + second_of(j) - 4];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       double sn = 0.0, cs = 1.0;
-      if (ROT != ROT_NONE && turns) turn_of(a, row, 4 * c + j, sn, cs);
-      double wu = 1.0, wv = 1.0;
-      if (weight) {
-        wu = (double)weight[first_of(j) < 4 ? lo + first_of(j) : hi + first_of(j) - 4];
-        wv = (double)weight[second_of(j) < 4 ? lo + second_of(j) : hi + second_of(j) - 4];
+      if constexpr (ROT != ROT_NONE) {
+        angle[j].turn(sn, cs);
+        sn = turns ? sn : 0.0;
+        cs = turns ? cs : 1.0;
       }
-      cu[j] = wu * cs;
-      sv[j] = wv * sn;
-      su[j] = wu * sn;
-      cv[j] = wv * cs;
+      cu[j] = (double)wu[j] * cs;
+      sv[j] = (double)wv[j] * sn;
+      su[j] = (double)wu[j] * sn;
+      cv[j] = (double)wv[j] * cs;
     }
   }
   __device__ __forceinline__ void apply(double y[8], double r) const {
@@ -165,6 +184,8 @@ struct AnyPairs {
   bool turns[8];
 
   __device__ __forceinline__ void form(const RopeArgs& a, int64_t row, const float* weight, int c, int, int) {
+    Angle angle[8];
+    float own[8], other[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int ch = 8 * c + j;
@@ -172,10 +193,20 @@ struct AnyPairs {
       const int pair = ROT == ROT_ANY_HALVES ? (upper ? ch - a.pairs : ch) : ch >> 1;
       turns[j] = pair < a.pairs;
       from[j] = !turns[j] ? ch : ROT == ROT_ANY_HALVES ? (upper ? pair : ch + a.pairs) : ch ^ 1;
-      double sn = 0.0, cs = 1.0;
-      if (turns[j]) turn_of(a, row, pair, sn, cs);
-      A[j] = weight ? cs * (double)weight[ch] : cs;
-      B[j] = (upper ? sn : -sn) * (weight ? (double)weight[from[j]] : 1.0);
+      angle[j].load(a, row, turns[j] ? pair : 0);
+      own[j] = other[j] = 1.0f;
+      if (weight) {  // uniform
+        own[j] = weight[ch];
+        other[j] = weight[from[j]];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool upper = ROT == ROT_ANY_HALVES ? 8 * c + j >= a.pairs : j & 1;
+      double sn, cs;
+      angle[j].turn(sn, cs);
+      A[j] = (double)own[j] * (turns[j] ? cs : 1.0);
+      B[j] = (double)other[j] * (turns[j] ? (upper ? sn : -sn) : 0.0);
     }
   }
   // head: the raw channels of the head
