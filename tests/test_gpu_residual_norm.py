@@ -220,9 +220,9 @@ def test_rows_past_4_gib():
 
 @pytest.mark.parametrize("d", [64, 1152])
 def test_rows_far_apart(d):
-    """Strides that no 32-bit offset spans over the rows of a wave, of one matrix and of all."""
-    tokens, stride = 1030, (1 << 25) + 8
-    flat = torch.zeros((tokens - 1) * stride + d, dtype=torch.bfloat16, device=DEV)
+    """Strides at which a wave takes one row."""
+    tokens, stride = 7300 if d == 64 else 1900, (1 << 20) + 8
+    flat = torch.empty((tokens - 1) * stride + d, dtype=torch.bfloat16, device=DEV)
     far = flat.as_strided((tokens, d), (stride, 1))
     x, y = cref.bf16((tokens, d), 1), cref.bf16((tokens, d), 2)
     far.copy_(x.to(DEV))
@@ -243,8 +243,9 @@ def test_rows_far_apart(d):
 
 
 # pieces a lane and rows a wave: the choices of the launch at many rows
-@pytest.mark.parametrize("tokens,d", [(5000, 32), (5003, 96), (4101, 160), (6000, 512), (5001, 736), (4099, 800), (3001, 1152),
-                                      (9001, 1152), (5001, 1536), (4100, 1760), (2051, 2240), (1100, 2592), (1100, 3040)])
+@pytest.mark.parametrize("tokens,d", [(33001, 32), (17003, 96), (9101, 160), (18001, 256), (33000, 128), (7301, 512), (17001, 512),
+                                      (3701, 736), (16385, 736), (7199, 800), (1801, 1152), (9001, 1152), (2801, 1536),
+                                      (4100, 1760), (2051, 2240), (1100, 2592), (1100, 3040)])
 def test_many_rows(tokens, d):
     g = torch.Generator().manual_seed(d)
     x = (torch.randn((tokens, d), generator=g)).to(torch.bfloat16)

@@ -560,9 +560,9 @@ const void* const wide_kernels[3][2][4] = {{KQ_WIDE(1, true, 1024, false), KQ_WI
 hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
   NormArgs a = args;
   a.inv_d = 1.0 / a.d;
-  // strides past what offsets between the rows of a wave hold
+  // rows so far apart that the offsets between those of a wave might not hold 31 bits have a wave each
   const int64_t most = std::max({a.x_stride, a.y ? a.y_stride : 0, a.y ? a.x_out_stride : 0, a.h ? a.h_stride : 0});
-  const bool far = most > int64_t(1) << 25;
+  const bool far = most > int64_t(1) << 20;
   const int64_t pieces = a.d / 8, cus = cu_count();
   void* kargs[] = {&a};
   if (pieces > 128 * kMaxWaves) {
@@ -573,9 +573,19 @@ hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
   const void* fn;
   int threads;
   int64_t rows, slots;  // rows of a step of a wave; workgroups that run at once
-  if (pieces <= 64 || (pieces <= 64 * kMaxPieces && a.tokens > 4 * cus && a.sample_rows >= 64)) {
-    // The fewest instructions: some 225 a piece of a lane and 120 for a row's sums, for all rows of a wave, and of
-    // waves as many as run at once do in one turn.  8192 rows of 1152: 2 rows a wave with 5 pieces TODO
+  // A row to a workgroup: 16 waves run on a compute unit, and workgroups are dealt to its four SIMDs from the first on,
+  // so that 3 waves take the room of 4 and 5 that of 8.
+  const int64_t wide_per = pieces <= 64 * kMaxWaves ? 1 : 2;
+  const int64_t waves = (pieces + 64 * wide_per - 1) / (64 * wide_per);
+  const int64_t room = waves > 2 ? (waves + 3) / 4 * 4 : waves;
+  // A row to a wave where there are rows for it: measured (us, norms on both sides, to codes; rows to waves and to
+  // workgroups) 512 channels 4096 rows 9.1 and 7.7, 8192 12.0 and 12.3; 736 channels 4096 rows 12.0 and 12.0; 1152
+  // channels 1536 rows 9.0 and 9.2, 4096 14.0 and 18.0; 2240 channels 1024 rows 10.9 and 10.2, 2048 13.4 and 17.6. And
+  // where a sample has rows for the waves of a workgroup, whose vectors are its own.
+  if (pieces <= 64 * kMaxPieces && a.tokens * room > 28 * cus && a.sample_rows >= 64) {
+    // Rows of a wave and pieces of a lane by the fewest instructions: some 225 a piece and 120 for a row's sums, which
+    // all rows of a wave share, as long as there are waves for the GPU. 8192 rows of 1152 (144 pieces): 2 rows a wave
+    // with 5 pieces a lane 19.2 us, one row with 3 pieces 21.3.
     int log = 6;
     double best = 0.0;
     for (int l = 6; l >= 2; --l) {
@@ -593,14 +603,11 @@ hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
     rows = 64 >> log;
     slots = cus * resident_per_cu(fn, threads);
   } else {
-    const int64_t per = pieces <= 64 * kMaxWaves ? 1 : 2;
-    const int64_t waves = (pieces + 64 * per - 1) / (64 * per);
     threads = (int)(64 * waves);
-    fn = wide_kernels[per == 1 ? 0 : threads <= 768 ? 1 : 2][a.y != nullptr][(a.h ? OUT_ROWS : 0) | (a.codes ? OUT_CODES : 0)];
+    fn = wide_kernels[wide_per == 1 ? 0 : threads <= 768 ? 1 : 2][a.y != nullptr]
+                     [(a.h ? OUT_ROWS : 0) | (a.codes ? OUT_CODES : 0)];
     rows = 1;
-    // workgroups are dealt to the four SIMDs of a compute unit from the first on: 5 waves take the room of 8
-    const int64_t room = 16 / ((waves + 3) / 4 * 4);
-    slots = cus * (room > 1 ? room : 1);
+    slots = cus * std::max<int64_t>(16 / room, 1);
   }
   // the same number of rows, of whole waves, for each workgroup that runs at once
   a.group_rows = ((a.tokens + slots - 1) / slots + rows - 1) / rows * rows;
