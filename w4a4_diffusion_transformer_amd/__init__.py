@@ -366,6 +366,7 @@ def _stream_object(stream, dev: int):
 
 
 _I32 = (torch.int32,)
+_F64 = (torch.float64,)
 _PAGE = 1 << 24  # slots of a page at most
 
 
@@ -513,19 +514,24 @@ def rope_freqs(axis_dims, base: float = 10000.0, device="cuda") -> torch.Tensor:
     return torch.cat([float(base) ** (-torch.arange(0, a, 2, dtype=torch.float64) / a) for a in axis_dims]).to(device)
 
 
+@functools.lru_cache(maxsize=256)
+def _axes(dims: tuple):
+    """Number of axes, their channels for the C struct, and the pairs that turn."""
+    if len(dims) > 4:
+        raise ValueError(f"axis_dims: at most 4 axes, got {len(dims)}")
+    if any(not 0 < a <= 128 or a % 2 for a in dims):
+        raise ValueError(f"axis_dims: even numbers from 2 to 128, got {dims}")
+    return len(dims), (ctypes.c_int32 * 4)(*dims), sum(dims) // 2
+
+
 def _rotation(rotation, tokens: int, dev: int):
     """The C struct of a Rotation (None stays None), its tensors checked."""
     if rotation is None:
         return None
-    dims = rotation.axis_dims
-    n = len(dims)
-    if n > 4:
-        raise ValueError(f"axis_dims: at most 4 axes, got {n}")
-    if any(not 0 < a <= 128 or a % 2 for a in dims):
-        raise ValueError(f"axis_dims: even numbers from 2 to 128, got {tuple(dims)}")
-    return _CRotation(_full(rotation.positions, "positions", _I32, (tokens, n), dev),
-                      _full(rotation.freqs, "freqs", (torch.float64,), (sum(dims) // 2,), dev), n,
-                      (ctypes.c_int32 * 4)(*dims), KQ_ROPE_HALVES if rotation.halves else KQ_ROPE_PAIRS)
+    positions, freqs, dims, halves = rotation
+    n, channels, pairs = _axes(tuple(dims))
+    return _CRotation(_full(positions, "positions", _I32, (tokens, n), dev), _full(freqs, "freqs", _F64, (pairs,), dev), n,
+                      channels, KQ_ROPE_HALVES if halves else KQ_ROPE_PAIRS)
 
 
 def _head_dim(width: int, heads: int, what: str) -> int:
@@ -545,7 +551,7 @@ def kq_rope(X, out, heads: int, rotation: Rotation | None = None, norm: int = KQ
     o, os_ = _rows(out, "out", width, tokens, dev)
     turn = _rotation(rotation, tokens, dev)
     _call(lib().kq_rope, "kq_rope", dev, stream, x, xs, tokens, heads, dim, norm,
-          _full(weight, "weight", _F32, (dim,), dev), eps, None if turn is None else ctypes.addressof(turn), o, os_)
+          _full(weight, "weight", _F32, (dim,), dev), eps, None if turn is None else ctypes.byref(turn), o, os_)
     return out
 
 
@@ -567,7 +573,7 @@ def kq_cache_write_rope(K, V, slots, k_codes, k_scales, v_codes, v_scales, kv_he
     turn = _rotation(rotation, tokens, dev)
     _call(lib().kq_cache_write_rope, "kq_cache_write_rope", dev, stream, q, qs, q_heads,
           _full(q_weight, "q_weight", _F32, (dim,), dev), o, os_, k, ks, v, vs, tokens, kv_heads, dim, norm,
-          _full(k_weight, "k_weight", _F32, (dim,), dev), eps, None if turn is None else ctypes.addressof(turn), at, n,
+          _full(k_weight, "k_weight", _F32, (dim,), dev), eps, None if turn is None else ctypes.byref(turn), at, n,
           *pools)
     return k_codes, k_scales, v_codes, v_scales
 
@@ -585,21 +591,21 @@ def kq_residual_norm(X, Y, x_out, post: int = KQ_NORM_NONE, post_weight=None, ga
     tokens, d = X.shape
     dev = _device(X, "X")
     per = tokens if tokens_per_sample is None else int(tokens_per_sample)
-    sampled = gate is not None or mod_scale is not None or mod_shift is not None
-    if sampled and per <= 0 < tokens:
+    if per <= 0 < tokens:
         raise ValueError("tokens_per_sample must be positive")
 
-    def rows(t, what):
-        return (None, d) if t is None else _rows(t, what, d, tokens, dev)
-
-    def vectors(t, what):
-        return None if t is None else _full(t, what, _F32, (-(-tokens // per) if tokens else t.shape[0], d), dev)
-
-    _call(lib().kq_residual_norm, "kq_residual_norm", dev, stream, *rows(X, "X"), *rows(Y, "Y"), tokens, d, post,
-          _full(post_weight, "post_weight", _F32, (d,), dev), vectors(gate, "gate"), residual_scale,
-          *rows(x_out, "x_out"), pre, _full(pre_weight, "pre_weight", _F32, (d,), dev), vectors(mod_scale, "mod_scale"),
-          vectors(mod_shift, "mod_shift"), per or 1, eps, *rows(h, "h"),
-          _full(out_codes, "out_codes", _U8, (tokens, d // 2), dev),
+    vectors = (-(-tokens // per) if tokens else 0, d)
+    if not tokens:  # nothing is read: any number of samples
+        gate = mod_scale = mod_shift = None
+    x, xs = _rows(X, "X", d, tokens, dev)
+    y, ys = (None, d) if Y is None else _rows(Y, "Y", d, tokens, dev)
+    o, os_ = (None, d) if x_out is None else _rows(x_out, "x_out", d, tokens, dev)
+    n, ns = (None, d) if h is None else _rows(h, "h", d, tokens, dev)
+    _call(lib().kq_residual_norm, "kq_residual_norm", dev, stream, x, xs, y, ys, tokens, d, post,
+          _full(post_weight, "post_weight", _F32, (d,), dev), _full(gate, "gate", _F32, vectors, dev), residual_scale,
+          o, os_, pre, _full(pre_weight, "pre_weight", _F32, (d,), dev),
+          _full(mod_scale, "mod_scale", _F32, vectors, dev), _full(mod_shift, "mod_shift", _F32, vectors, dev), per or 1,
+          eps, n, ns, _full(out_codes, "out_codes", _U8, (tokens, d // 2), dev),
           _full(out_scales, "out_scales", _U8, (tokens, d // 32), dev),
           _full(row_stats, "row_stats", _F32, (tokens, 2), dev))
     return x_out, h
