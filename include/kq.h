@@ -498,8 +498,9 @@ typedef struct {
  * (elements, a multiple of 8), 16-byte aligned; out may be X itself at the
  * same stride, or other columns of the same matrix; any other overlap is
  * KQ_ERR_ALIAS.  KQ_NORM_LAYER and unknown layouts are KQ_ERR_VARIANT; axes
- * that are odd, negative or more than head_dim together KQ_ERR_SHAPE.
- * weight and positions 4-byte, freqs 8-byte aligned.
+ * that are odd, negative or more than head_dim together KQ_ERR_SHAPE, as are
+ * more than 2^21 heads or 2^24 channels.  weight and positions 4-byte, freqs
+ * 8-byte aligned.  A row of zeros with eps 0 is NaN, as the formula's.
  */
 kq_status kq_rope(const uint16_t* X, int64_t X_stride, int64_t tokens, int64_t heads, int64_t head_dim, kq_norm norm,
                   const float* weight, float eps, const kq_rotation* rotation, uint16_t* out, int64_t out_stride,
