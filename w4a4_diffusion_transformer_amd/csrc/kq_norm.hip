@@ -21,6 +21,21 @@
 //          a wave, for few rows, and for samples of few rows;
 //   long   a row to a workgroup, read from memory again for each step.
 // In the first two each row of x and y is read once.
+//
+// What bounds it, measured (kernel alone; a copy reaches 5.09 TB/s).  Many
+// rows: memory.  18432 x 2240, RMS norms on both sides, gate, modulation, rows:
+// 70 to 75 us, 4.4 to 4.7 TB/s.  Where each wave has one step, vectors, rows,
+// sums and stores follow one another on all of the GPU at once: 8192 x 1152 to
+// codes 19 us, of them 9 of instructions; 4097 x 2240 to statistics 14.4.  Wide
+// rows, one workgroup a compute unit: 1009 x 12288 to codes 24.8 us, 15 of
+// instructions and two barriers a row beside 16 of memory.  Few rows (8 x
+// 2240): the launch and one row's chain, 4.8 us.
+//
+// Cache policy.  What the next kernel reads is stored as usual: past the caches
+// this one would end sooner, but with the reader behind it the two take longer
+// (8192 x 1152 to codes, and the codes read: 25.3 us and 27.2).  The stream,
+// where h or codes are what the next kernel reads, is not touched again before
+// the block ends and passes the caches by (24.3; 1009 x 12288 35.6 and 32.6).
 #include <algorithm>
 
 #include "kq_device.hpp"
@@ -43,19 +58,15 @@ constexpr int kMaxPieces = 6;      // of a lane of the rows kernel
 constexpr int kRowsThreads = 512;  // of its workgroups
 constexpr int kLong = 1024;  // threads of a workgroup whose rows stay in memory
 
-// This lane's pieces of a wave's rows, P pieces `step` bytes apart: of one row, a buffer of its own (address in scalar
-// registers, pieces past its end read as zero and are not written), or with LOG < 6 of row `sub` of several rows
-// `stride` bytes apart in one buffer.  `there`: which lanes have their pieces but the last, and the last (LOG < 6).
+// A lane's place: its row of the wave's (LOG < 6) and its piece, and whether it has its pieces but the last, and the last.
 struct Lane {
   int sub, piece;
   bool there, last;
 };
 
-//
-// Cache policy.  What the next kernel reads is stored as usual: past the caches this one would end sooner, but with the
-// reader behind it the two take longer (8192 x 1152 to codes, and the codes read: 25.3 us and 27.2).  The stream, where
-// h or codes are what the next kernel reads, is not touched again before the block ends and passes the caches by (24.3;
-// 1009 x 12288 35.6 and 32.6).
+// This lane's pieces of a wave's rows, P pieces `step` bytes apart: of one row, a buffer of its own (address in scalar
+// registers, pieces past its end read as zero and are not written), or with LOG < 6 of row `sub` of several rows
+// `stride` bytes apart in one buffer.
 template <int LOG, int P>
 struct Rows {
   __amdgpu_buffer_rsrc_t r;

@@ -21,6 +21,15 @@
 // kq_cache_write's do.  Values are taken as that call takes them.  R that is no
 // multiple of 8 takes a slower form: a lane holds a piece and fetches each
 // partner.
+//
+// What bounds it, measured (kernel alone; a copy reaches 5.09 TB/s).  Many
+// tokens: memory.  32761 tokens of 16 heads of 128, three axes, norm: 56 us,
+// 4.75 TB/s; 20481 tokens of 32 queries, 8 keys and 8 values of 128 to the
+// cache: 98 us, 4.5 TB/s.  Some thousand tokens: a wave's chain of position,
+// frequency, sines, heads and, for keys, the way through LDS, which all waves
+// go through at the same time.  8192 tokens of 16 heads of 72: 10.8 us, a copy
+// 6.5; 4095 of 16 keys and values of 72: 13.4 us.  A few tokens: the launch and
+// that chain, 4.7 to 4.9 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -414,7 +423,10 @@ hipError_t launch_rope(const RopeArgs& args, hipStream_t stream) {
     const int64_t row_bytes = 2 * std::max(p.x_stride, p.codes ? 0 : p.out_stride);
     p.tokens = (int)std::clamp<int64_t>((int64_t(1) << 30) / row_bytes, 1, 64 / pieces);
     const int64_t tiles = (a.tokens + p.tokens - 1) / p.tokens;
-    // heads of a wave: all of its tokens', or fewer (but whole blocks of 32) where that leaves the GPU idle
+    // Heads of a wave: all of its tokens', or fewer (but whole blocks of 32) where there would be less than 8 waves a
+    // compute unit. Aimed at 2, 4, 8 and 16 waves (us): 8192 tokens of 16 heads of 72 11.2, 11.3, 11.3 and 13.0, 4095
+    // tokens of 16 keys and values of 72 22, 17, 14.5 and 14.3, 6001 tokens of 20 + 10 + 10 heads of 96 22.1, 22.6, 21.8
+    // and 24.1: fewer leave the GPU idle, more form the same sines again.
     int unit = 1;
     while (p.codes && unit * a.head_dim % 32 != 0) ++unit;
     const int64_t units = (p.heads + unit - 1) / unit;
