@@ -9,7 +9,11 @@
 // arithmetic up to each rounding are fp64: a norm is fma(x, rstd, -mean rstd)
 // and the vectors are folded into one factor before x' and a factor and a term
 // after it.  sum (x - mean)^2 is taken as sum x^2 - mean sum x where that
-// keeps 2^-40, else in a second pass.
+// keeps 2^-40, else in a second pass.  A channel that equals the mean has to
+// come out as 0, or MXFP4 gives a block of them a scale and codes: the mean is
+// the sum's correctly rounded quotient, and rstd keeps 45 bits, with which its
+// product with a mean that is a bf16 value (8 bits) is exact.  (x - mean) rstd
+// would do that too: 8192 x 1152 19.4 us for 19.0, 18432 x 2240 75.3 for 74.2.
 //
 // Layout.  A lane holds 16-byte pieces of a row; four adjacent lanes hold a
 // block of 32.  Three kernels:
@@ -236,7 +240,12 @@ template <class Sum, class Again>
 __device__ __forceinline__ Norm settle(const NormArgs& a, int kind, double s, double q, Sum& sum, Again&& again) {
   Norm n;
   sum(s, q);
-  n.mean = kind == 2 ? s * a.inv_d : 0.0;
+  if (kind == 2) {
+    // s / d, correctly rounded: the product with the rounded reciprocal, corrected by its exact remainder
+    n.mean = s * a.inv_d;
+    const double m = fma(fma(-n.mean, (double)a.d, s), a.inv_d, n.mean);
+    n.mean = m == m ? m : n.mean;  // an infinite sum has no remainder
+  }
   double m2 = kind == 2 ? q - s * n.mean : q;  // s of an infinite row may be NaN
   const bool cancels = kind == 2 && m2 * 0x1p12 < q;
   // the whole wave (and, as sums are equal in all of them, the workgroup) if any row of it
@@ -252,6 +261,8 @@ __device__ __forceinline__ Norm settle(const NormArgs& a, int kind, double s, do
     m2 = cancels ? far : m2;
   }
   n.rstd = inverse_sqrt(fma(m2, a.inv_d, a.eps));
+  // less by 2^-44 of itself at most; mean rstd is exact where a channel can equal the mean
+  n.rstd = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, n.rstd) & ~uint64_t(0xFF));
   n.shift = kind == 2 ? -n.mean * n.rstd : -0.0;
   return n;
 }
