@@ -259,3 +259,28 @@ def test_more_heads_than_a_round_of_the_gpu():
         out = torch.empty_like(x, device=DEV)
         kq.kq_rope(x.to(DEV), out, heads, on_gpu(rotation), kq.KQ_NORM_RMS)
         ref.check(out, *ref.rope(x, heads, rotation, True))
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("axes", [(6,), (10, 4), (8,), ()])
+def test_channels_that_do_not_turn(halves, axes):
+    """They come out as they are, the sign of a zero with them; an infinite weight of one makes that one infinite."""
+    tokens, heads, dim, R = 5, 3, 64, sum(axes)
+    x = cref.bf16((tokens, heads * dim), 5)
+    x.view(tokens, heads, dim)[:, :, 20:40:3] = -0.0
+    x.view(tokens, heads, dim)[:, :, 21:40:3] = 0.0
+    rotation = turn(tokens, axes, halves, 3) if axes else None
+    out = torch.empty_like(x, device=DEV)
+    kq.kq_rope(x.to(DEV), out, heads, on_gpu(rotation))
+    kept = lambda t: t.cpu().view(torch.int16).view(tokens, heads, dim)[:, :, R:]
+    assert torch.equal(kept(out), kept(x))
+    ref.check(out, *ref.rope(x, heads, rotation))
+    w = weights(dim, 4)
+    w[41], w[44], w[50] = float("inf"), -float("inf"), -1.0
+    kq.kq_rope(x.to(DEV), out, heads, on_gpu(rotation), kq.KQ_NORM_RMS, w.to(DEV))
+    want = ref.rope(x, heads, rotation, True, w)
+    assert torch.isinf(want[0]).sum() == 2 * tokens * heads
+    ref.check(out, *want)
+    zero = x.view(tokens, heads, dim)[:, :, 20:40] == 0
+    assert torch.equal(torch.signbit(out.cpu().view(tokens, heads, dim)[:, :, 20:40][zero]),
+                       torch.signbit(x.view(tokens, heads, dim)[:, :, 20:40][zero]))

@@ -215,14 +215,15 @@ struct AnyPairs {
       double sn, cs;
       angle[j].turn(sn, cs);
       A[j] = (double)own[j] * (turns[j] ? cs : 1.0);
-      B[j] = (double)other[j] * (turns[j] ? (upper ? sn : -sn) : 0.0);
+      B[j] = turns[j] ? (double)other[j] * (upper ? sn : -sn) : 0.0;  // an infinite weight's product would be NaN
     }
   }
   // head: the raw channels of the head
   __device__ __forceinline__ void apply(double y[8], double r, const uint16_t* head) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const double other = turns[j] ? (double)__uint_as_float((unsigned)head[from[j]] << 16) : 0.0;
+      // -0 leaves a channel that does not turn its sign
+      const double other = turns[j] ? (double)__uint_as_float((unsigned)head[from[j]] << 16) : -0.0;
       y[j] = fma(B[j], other, A[j] * y[j]) * r;
     }
   }
