@@ -154,3 +154,10 @@ def test_rope_freqs():
     f = kq.rope_freqs((4, 6), 100.0, "cpu")
     want = torch.tensor([1.0, 100.0 ** -0.5, 1.0, 100.0 ** (-1 / 3), 100.0 ** (-2 / 3)], dtype=torch.float64)
     assert f.dtype == torch.float64 and torch.allclose(f, want, rtol=1e-15, atol=0)
+
+
+def test_absurd_head_dims(lib):
+    """Refused before a product with the number of heads is formed, which would pass 63 bits."""
+    for dim in ((1 << 62) + 8, 1 << 62, -(1 << 62), (1 << 60) + 64, (1 << 63) - 8):
+        assert rope(lib, heads=1 << 21, dim=dim) == SHAPE
+        assert append(lib, hk=1 << 21, dim=dim) == append(lib, hq=1 << 21, dim=dim) == SHAPE

@@ -362,15 +362,18 @@ kq_status run_cache(bool write, const uint16_t* k, int64_t k_stride, const uint1
   return from_hip(kq::launch_cache(write, v != nullptr, a, stream));
 }
 
+// Heads whose channels can be counted (their product is formed after this).
+bool good_heads(int64_t heads, int64_t head_dim) {
+  return heads > 0 && heads <= (int64_t(1) << 21) && head_dim > 0 && head_dim <= 128 && head_dim % 8 == 0;
+}
+
 // Shared body of kq_rope (queries alone) and kq_cache_write_rope (V and Q may be missing).
 kq_status run_rope(const Rows& q, int64_t q_heads, const float* q_weight, const Rows& q_out, const Rows& k, const Rows& v,
                    int64_t tokens, int64_t kv_heads, int64_t head_dim, kq_norm norm, const float* k_weight, float eps,
                    const kq_rotation* rotation, const int32_t* slots, int64_t n_slots, uint8_t* kc, uint8_t* ks,
                    uint8_t* vc, uint8_t* vs, hipStream_t stream) {
   const bool cache = kv_heads > 0;
-  if (head_dim <= 0 || head_dim > 128 || head_dim % 8 != 0) return KQ_ERR_SHAPE;
   for (int64_t heads : {q_heads, kv_heads}) {
-    if (heads > (int64_t(1) << 21)) return KQ_ERR_SHAPE;
     if (heads == 0) continue;
     // check_shape for whole blocks of 32; rows that are not quantized need not be
     const kq_status st = check_shape(tokens, (heads * head_dim + 31) / 32 * 32);
@@ -699,7 +702,7 @@ kq_status kq_cache_read(const uint8_t* K_codes, const uint8_t* K_scales, const u
 kq_status kq_rope(const uint16_t* X, int64_t X_stride, int64_t tokens, int64_t heads, int64_t head_dim, kq_norm norm,
                   const float* weight, float eps, const kq_rotation* rotation, uint16_t* out, int64_t out_stride,
                   hipStream_t stream) {
-  if (heads <= 0 || heads > (int64_t(1) << 24)) return KQ_ERR_SHAPE;
+  if (!good_heads(heads, head_dim)) return KQ_ERR_SHAPE;
   const int64_t width = heads * head_dim;
   return run_rope({X, X_stride, width}, heads, weight, {out, out_stride, width}, {}, {}, tokens, 0, head_dim, norm,
                   nullptr, eps, rotation, nullptr, 0, nullptr, nullptr, nullptr, nullptr, stream);
@@ -711,8 +714,7 @@ kq_status kq_cache_write_rope(const uint16_t* Q, int64_t Q_stride, int64_t q_hea
                               kq_norm norm, const float* k_weight, float eps, const kq_rotation* rotation,
                               const int32_t* slots, int64_t n_slots, uint8_t* K_codes, uint8_t* K_scales,
                               uint8_t* V_codes, uint8_t* V_scales, hipStream_t stream) {
-  if (kv_heads <= 0 || kv_heads > (int64_t(1) << 24) || (Q && (q_heads <= 0 || q_heads > (int64_t(1) << 24))))
-    return KQ_ERR_SHAPE;
+  if (!good_heads(kv_heads, head_dim) || (Q && !good_heads(q_heads, head_dim))) return KQ_ERR_SHAPE;
   if (!Q) q_heads = 0;
   const int64_t q_width = q_heads * head_dim, width = kv_heads * head_dim;
   return run_rope({Q, Q_stride, q_width}, q_heads, Q ? q_weight : nullptr, {Q ? Q_out : nullptr, Q_out_stride, q_width},
