@@ -7,7 +7,10 @@
 #include <cstdlib>
 #include <cmath>
 #include <cstring>
+#include <map>
 #include <mutex>
+#include <new>
+#include <tuple>
 #include <vector>
 
 #include "kq.h"
@@ -509,25 +512,23 @@ int cu_count() {
 }
 
 int resident_per_cu(const void* fn, int block_threads) {
-  struct Entry {
-    const void* fn;
-    int dev, threads, value;
-  };
   static std::mutex mu;
-  static Entry table[64];
-  static int used = 0;
+  static std::map<std::tuple<int, const void*, int>, int> known;  // a process may use every kernel on every GPU
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) dev = 0;
   int value = 0;
   {
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; ++i)
-      if (table[i].fn == fn && table[i].dev == dev && table[i].threads == block_threads) value = table[i].value;
-    if (value == 0) {
-      int n = 0;
-      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, block_threads, 0) != hipSuccess || n <= 0) n = 1;
-      value = n;
-      if (used < 64) table[used++] = Entry{fn, dev, block_threads, value};
+    const std::tuple<int, const void*, int> key{dev, fn, block_threads};
+    const auto at = known.find(key);
+    if (at != known.end()) {
+      value = at->second;
+    } else {
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&value, fn, block_threads, 0) != hipSuccess || value <= 0) value = 1;
+      try {
+        known.emplace(key, value);
+      } catch (const std::bad_alloc&) {  // asked again next time
+      }
     }
   }
   const int cap = overrides().wg_per_cu;
