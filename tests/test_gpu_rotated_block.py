@@ -302,3 +302,100 @@ def test_refusals_with_tensors():
         with pytest.raises(kq.KQError) as e:
             call()
         assert e.value.status == status
+
+
+def written(thing):
+    """Everything that a run writes."""
+    if isinstance(thing, Step):
+        return [thing.x, thing.qo, *thing.cache, *thing.codes]
+    return [thing.x, thing.stats, thing.q, thing.att, thing.h1, thing.qkv, thing.y1, thing.h, thing.y2, thing.lse, *thing.cache,
+            *(t for pair in thing.codes.values() for t in pair)]
+
+
+def poison(thing):
+    for t in written(thing):
+        t.view(torch.uint8).fill_(0xA5)
+
+
+def expected(thing):
+    """What a run leaves behind in poisoned buffers (slots without a token keep the poison)."""
+    poison(thing)
+    thing.run()
+    torch.cuda.synchronize()
+    return [t.clone() for t in written(thing)]
+
+
+@pytest.mark.parametrize("kind", [Block, Step])
+def test_replays_write_everything(kind):
+    a, b = kind(51), kind(52)
+    want = [expected(t) for t in (a, b)]
+    ga, gb = capture(a), capture(b)
+    for _ in range(3):
+        poison(a)
+        poison(b)
+        ga.replay()
+        gb.replay()
+        torch.cuda.synchronize()
+        assert same(written(a), want[0]) and same(written(b), want[1])
+
+
+def test_threads_write_everything():
+    things = [Step(60), Block(61), Step(62), Block(63)]
+    want = [expected(t) for t in things]
+    streams, got = [torch.cuda.Stream() for _ in things], [[] for _ in things]
+    errors = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(4):
+                    poison(things[i])
+                    things[i].run()
+                    got[i].append([t.clone() for t in written(things[i])])
+        except Exception as e:  # reported below, in the main thread
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(things))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert all(same(g, want[i]) for i in range(len(things)) for g in got[i])
+
+
+@pytest.mark.parametrize("given", ["stream", "address", "default"])
+def test_the_stream_given_orders_the_calls(given):
+    """The inputs come to be on the stream given, behind long work, and are not there yet when the calls are made from
+    another current stream; what the calls wrote is copied on the stream given."""
+    t = Step(70)
+    want = expected(t)
+    inputs = (t.qkv, t.start, t.y)
+    good = [x.clone() for x in inputs]
+    m = torch.randn((8192, 8192), device=DEV)
+    out = torch.empty_like(m)
+    s = torch.cuda.default_stream() if given == "default" else torch.cuda.Stream()
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.mm(m, m, out=out)
+    poison(t)
+    for x in inputs:
+        x.fill_(float("nan"))
+    torch.cuda.synchronize()
+    ready = torch.cuda.Event()
+    with torch.cuda.stream(s):
+        for _ in range(12):
+            torch.mm(m, m, out=out)
+        for x, g in zip(inputs, good):
+            x.copy_(g)
+        ready.record()
+    with torch.cuda.stream(other):
+        t.run(stream={"stream": s, "address": s.cuda_stream, "default": 0}[given])
+    early = not ready.query()
+    with torch.cuda.stream(s):
+        got = [x.clone() for x in written(t)]
+    torch.cuda.synchronize()
+    assert early, "the work in front was over too soon for this test to say anything"
+    assert same(got, want)
