@@ -492,9 +492,10 @@ typedef struct {
  *   n = x                                        norm KQ_NORM_NONE, or
  *   n = x weight / sqrt(mean(x^2) + eps)         KQ_NORM_RMS (weight fp32 [head_dim], NULL: 1);
  *   (u, v) of a pair -> (u cos a - v sin a, u sin a + v cos a),
- * rounded once to bf16: everything before is fp64, the angles too, so far
- * positions keep theirs (to 2^-52 of the angle, and 2^-40).  X and out are
- * bf16 [tokens][heads * head_dim] at strides X_stride and out_stride
+ * rounded once to bf16 (below 2^-126 by way of fp32's last step, 2^-149):
+ * everything before is fp64, the angles too, so far positions keep theirs (to
+ * 2^-51 of the angle, and 2^-40).  X and out are bf16
+ * [tokens][heads * head_dim] at strides X_stride and out_stride
  * (elements, a multiple of 8), 16-byte aligned; out may be X itself at the
  * same stride, or other columns of the same matrix; any other overlap is
  * KQ_ERR_ALIAS.  KQ_NORM_LAYER and unknown layouts are KQ_ERR_VARIANT; axes
@@ -538,9 +539,11 @@ kq_status kq_cache_write_rope(const uint16_t* Q, int64_t Q_stride, int64_t q_hea
  *                                                      kq_quantize_adaln reads to transform and quantize x'
  * with the norms of kq_norm over the row's d channels, statistics of x' taken
  * from the bf16 values that are stored, and samples = ceil(tokens /
- * tokens_per_sample).  Arithmetic and sums are fp64 up to each rounding.  h is
- * rounded once, so it may differ by a bf16 step from what kq_quantize_adaln
- * forms in fp32 steps.
+ * tokens_per_sample).  Arithmetic and sums are fp64 up to each rounding
+ * (roundings to bf16 as kq_rope's); a channel that equals its row's mean is 0
+ * after a layer norm.  Statistics may differ from kq_row_stats' by an fp32
+ * step, where a sum lies next to a tie.  h is rounded once, so it may differ by
+ * a bf16 step from what kq_quantize_adaln forms in fp32 steps.
  *
  * Y NULL: the stream is X as it is (x' = x, the first block's norm): X_out,
  * post, post_weight, gate have to be NULL / KQ_NORM_NONE and residual_scale 1

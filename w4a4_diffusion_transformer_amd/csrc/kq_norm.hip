@@ -30,16 +30,20 @@
 // rows: memory.  18432 x 2240, RMS norms on both sides, gate, modulation, rows:
 // 70 to 75 us, 4.4 to 4.7 TB/s.  Where each wave has one step, vectors, rows,
 // sums and stores follow one another on all of the GPU at once: 8192 x 1152 to
-// codes 19 us, of them 9 of instructions; 4097 x 2240 to statistics 14.4.  Wide
-// rows, one workgroup a compute unit: 1009 x 12288 to codes 24.8 us, 15 of
-// instructions and two barriers a row beside 16 of memory.  Few rows (8 x
-// 2240): the launch and one row's chain, 4.8 us.
+// codes 19 us, of them 9 of instructions, and 12 without Y; 4097 x 2240 to
+// statistics 14.5.  Wide rows, one workgroup a compute unit: 1009 x 12288 to codes
+// 25 us, 15 of instructions and two barriers a row beside 16 of memory; 1009 x
+// 24576, rows read again, 62 for 32 of memory.  Few rows (8 x 2240): the launch
+// and one row's chain, 4.8 to 4.9 us.
 //
 // Cache policy.  What the next kernel reads is stored as usual: past the caches
 // this one would end sooner, but with the reader behind it the two take longer
 // (8192 x 1152 to codes, and the codes read: 25.3 us and 27.2).  The stream,
 // where h or codes are what the next kernel reads, is not touched again before
 // the block ends and passes the caches by (24.3; 1009 x 12288 35.6 and 32.6).
+// Were it read next after all (two such norms in a row, 2240 channels): no
+// difference from 8 to 256 rows (8.8 and 8.8, 9.4 and 9.4 us), 4096 rows 41.0 for
+// 40.2, 18432 rows 136 for 127.
 #include <algorithm>
 
 #include "kq_device.hpp"
@@ -611,7 +615,12 @@ hipError_t launch_residual_norm(const NormArgs& args, hipStream_t stream) {
   // A row to a wave where there are rows for it: measured (us, norms on both sides, to codes; rows to waves and to
   // workgroups) 512 channels 4096 rows 9.1 and 7.7, 8192 12.0 and 12.3; 736 channels 4096 rows 12.0 and 12.0; 1152
   // channels 1536 rows 9.0 and 9.2, 4096 14.0 and 18.0; 2240 channels 1024 rows 10.9 and 10.2, 2048 13.4 and 17.6. And
-  // where a sample has rows for the waves of a workgroup, whose vectors are its own.
+  // where a sample has rows for the waves of a workgroup, whose vectors are its own: samples of 8, 16, 64 and 256 rows,
+  // layer norm, gate and modulation to codes, in waves 21.4, 19.1, 18.7, 18.5 and in workgroups 25.0, 24.4, 23.8, 22.9
+  // (8192 x 1152); 18.9, 18.8, 19.1, 18.3 and 23.3, 23.3, 23.3, 22.1 (4096 x 2240); 27.0, 17.7, 16.3, 16.2 and 18.2, 17.3,
+  // 15.8, 14.6 (16384 x 512); 31.2, 20.2, 10.2, 10.0 and 24.0, 23.9, 23.8, 23.9 (32768 x 96): wide rows would gain from 8
+  // on, narrow ones lose there. Samples of one row, in workgroups: 8192 x 1152 38 us, of them 34 of memory for rows and
+  // vectors; 16384 x 64 17, of them 4.
   if (pieces <= 64 * kMaxPieces && a.tokens * room > 28 * cus && a.sample_rows >= 64) {
     // Rows of a wave and pieces of a lane by the fewest instructions: some 225 a piece and 120 for a row's sums, which
     // all rows of a wave share, as long as there are waves for the GPU. 8192 rows of 1152 (144 pieces): 2 rows a wave

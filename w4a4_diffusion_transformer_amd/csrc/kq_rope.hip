@@ -27,9 +27,13 @@
 // 4.75 TB/s; 20481 tokens of 32 queries, 8 keys and 8 values of 128 to the
 // cache: 98 us, 4.5 TB/s.  Some thousand tokens: a wave's chain of position,
 // frequency, sines, heads and, for keys, the way through LDS, which all waves
-// go through at the same time.  8192 tokens of 16 heads of 72: 10.8 us, a copy
-// 6.5; 4095 of 16 keys and values of 72: 13.4 us.  A few tokens: the launch and
-// that chain, 4.7 to 4.9 us.
+// go through at the same time.  8192 tokens of 16 heads of 72: 10.4 to 10.8 us, a
+// copy 6.5.  4095 of 16 keys and values of 72, normalised: 13.8 to 14.2 us; the
+// keys alone 12.5, values alone 5.3, the same heads turned into rows 11.1, without
+// the norm 8.4: it is the keys' chain, the norm's sums a quarter of it.  A few
+// tokens: the launch and that chain, 4.7 to 4.9 us.  R that is no multiple of 8:
+// 32761 tokens as above 71 (neighbours) and 73 us (halves), every partner a
+// 16-bit read from LDS; 20481 as above 122 us.
 #include <algorithm>
 #include <type_traits>
 
